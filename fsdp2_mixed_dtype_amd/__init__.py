@@ -18,6 +18,10 @@ Functions (same names as the C ABI without the ``fsdppack_`` prefix):
   reduce_scatter_copy_out_all(plan, rank, rs_outs, shard_grads, divide_factor=1.0, stream=None)
                                                (every bucket's write-back in one launch)
 
+The training operators that make the gradients (the norm, 8-bit activation
+checkpoints, the weight gradient, the gated feed-forward block) are in
+``training.py`` and are reached from here under the same names.
+
 The tensor lists may also be given as a PointerArray from prepare_grads /
 prepare_shards / prepare_params / prepare_shard_grads: validated once and
 reused across calls, the way a training loop reuses its gradient and shard
@@ -473,3 +477,11 @@ def empty_launch(workgroups: int, threads: int = 64, stream=None):
     """Launch a kernel that does nothing with the given grid (the floor of a
     launch of that many workgroups; a measurement aid)."""
     _check(lib().fsdppack_empty_launch(int(workgroups), int(threads), _stream(stream)))
+
+
+# The training operators (norm, 8-bit activation checkpoints, weight gradient,
+# gated block) build on what is defined above.
+from .training import (CHECKPOINT_GROUP, E4M3, GELU_TANH, INT8, LAYER_NORM, RMS_NORM, SILU, Checkpoint,  # noqa: E402,F401
+                       checkpoint_empty, checkpoint_load, checkpoint_save, gated_backward, gated_backward_workspace,
+                       gated_forward, norm_backward, norm_backward_workspace, norm_forward, weight_grad,
+                       weight_grad_workspace)

@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfsdppack.so")
 ARCH = "gfx950"
 
-SOURCES = ["fsdppack_kernels.hip", "fsdppack_plan.cpp", "fsdppack_abi.cpp"]
+SOURCES = ["fsdppack_kernels.hip", "fsdppack_plan.cpp", "fsdppack_abi.cpp",
+           "fsdppack_train.hip", "fsdppack_gemm.hip", "fsdppack_train.cpp"]
 
 
 def hipcc() -> str:

@@ -20,6 +20,7 @@
 #include <string>
 
 #include "fsdppack_plan.h"
+#include "fsdppack_train.h"
 
 using namespace fsdppack;
 
@@ -329,6 +330,21 @@ int check_pack_args(const fsdppack_plan *plan, int32_t bucket, const void *const
 }
 
 }  // namespace
+
+// What the training operators' calls share with the ones here.
+namespace fsdppack {
+
+int report(int code, const std::string &msg) { return fail(code, msg); }
+int report_hip(int hip_error, const char *what) { return hip_fail(static_cast<hipError_t>(hip_error), what); }
+void take_timing_events(void **start, void **stop)
+{
+    const ArmedEvents ev = take_armed_events();
+    *start = ev.start;
+    *stop = ev.stop;
+}
+void count_launches(int64_t n) { g_counters[0] += n; }
+
+}  // namespace fsdppack
 
 extern "C" {
 

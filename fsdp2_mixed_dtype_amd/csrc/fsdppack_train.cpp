@@ -1,0 +1,488 @@
+// fsdppack_train.cpp -- the C ABI of the training operators (declared in
+// include/fsdppack.h): argument checks on the host, then their launches on
+// the caller's stream.  Nothing is allocated and nothing waits; scratch
+// memory is the caller's.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "fsdppack_train.h"
+
+using namespace fsdppack;
+
+namespace {
+
+constexpr int64_t kMaxCols = kMaxStride;
+constexpr int64_t kMaxRows = int64_t{1} << 38;
+
+bool eight_bit(int32_t dt) { return dt == FSDPPACK_E4M3 || dt == FSDPPACK_INT8; }
+bool dense(int32_t dt) { return dt == FSDPPACK_BF16 || dt == FSDPPACK_FP32; }
+int64_t size_of(int32_t dt) { return dt == FSDPPACK_FP32 ? 4 : dt == FSDPPACK_BF16 ? 2 : 1; }
+
+// Checks of one call's matrices.  The first failure is kept.
+struct Check {
+    const char *call;
+    int rc = FSDPPACK_OK;
+
+    bool fail(int code, const std::string &msg)
+    {
+        if (rc == FSDPPACK_OK) rc = report(code, std::string(call) + ": " + msg);
+        return false;
+    }
+
+    // m with the given shape, its dtype allowed by a set of bits (1 << dtype)
+    bool matrix(const fsdppack_matrix *m, const char *name, int64_t rows, int64_t cols, uint32_t dtypes, Mat *out)
+    {
+        if (rc != FSDPPACK_OK) return false;
+        auto bad = [&](int code, const char *what) { return fail(code, std::string(name) + " " + what); };
+        if (m == nullptr) return bad(FSDPPACK_EINVAL, "is NULL");
+        if (m->dtype < 0 || m->dtype > 31 || !(dtypes >> m->dtype & 1)) return bad(FSDPPACK_EDTYPE, "has an unsupported dtype");
+        if (m->rows != rows || m->cols != cols) return bad(FSDPPACK_EINVAL, "has another shape than the call needs");
+        const int64_t ld = rows > 1 ? m->stride : cols;
+        if (ld < cols) return bad(FSDPPACK_EINVAL, "has rows that overlap (stride below its columns)");
+        if (ld > kMaxStride) return bad(FSDPPACK_EINVAL, "has too wide a stride (over 2^21 elements)");
+        if (eight_bit(m->dtype) && ld != cols) return bad(FSDPPACK_EINVAL, "has 8-bit values that are not contiguous");
+        if (rows > 0 && (m->data == nullptr || reinterpret_cast<uintptr_t>(m->data) % size_of(m->dtype) != 0))
+            return bad(FSDPPACK_EINVAL, "has data that is NULL or not aligned to its element size");
+        if (rows > 0 && eight_bit(m->dtype) && m->scales == nullptr) return bad(FSDPPACK_EINVAL, "has no scales");
+        out->p = m->data;
+        out->scales = static_cast<uint8_t *>(m->scales);
+        out->ld = ld;
+        out->dt = m->dtype;
+        return true;
+    }
+
+    bool shape(const fsdppack_matrix *m, const char *name)
+    {
+        if (m == nullptr) return fail(FSDPPACK_EINVAL, std::string(name) + " is NULL");
+        if (m->rows < 0 || m->rows > kMaxRows || m->cols < 1 || m->cols > kMaxCols)
+            return fail(FSDPPACK_EINVAL, std::string(name) + " needs rows >= 0 and 1 to 2^21 columns");
+        return true;
+    }
+
+    bool vector(const void *p, int32_t dtype, const char *name)
+    {
+        if (rc != FSDPPACK_OK) return false;
+        if (p != nullptr && !dense(dtype)) return fail(FSDPPACK_EDTYPE, std::string(name) + " has an unsupported dtype");
+        if (p != nullptr && reinterpret_cast<uintptr_t>(p) % size_of(dtype) != 0)
+            return fail(FSDPPACK_EINVAL, std::string(name) + " is not aligned to its element size");
+        return true;
+    }
+};
+
+// Memory that a call reads or writes: `rows` pieces of `width` bytes, `pitch` apart.
+struct Span {
+    const char *p;
+    int64_t rows, width, pitch;
+    bool written;
+    const char *name;
+};
+
+struct Spans {
+    Span s[24];
+    int n = 0;
+
+    void put(const void *p, int64_t rows, int64_t width, int64_t pitch, bool written, const char *name)
+    {
+        if (p != nullptr && rows > 0 && width > 0) s[n++] = Span{static_cast<const char *>(p), rows, width, pitch, written, name};
+    }
+    void put(const Mat &m, int64_t rows, int64_t cols, bool written, const char *name)
+    {
+        const int64_t z = size_of(m.dt);
+        put(m.p, rows, cols * z, m.ld * z, written, name);
+        if (m.p != nullptr && eight_bit(m.dt)) put(m.scales, 1, rows * ((cols + kGroup - 1) / kGroup), 0, written, name);
+    }
+
+    // whether an output shares memory with anything else of the call
+    bool overlap(Check &c) const
+    {
+        for (int a = 0; a < n; ++a)
+            for (int b = a + 1; b < n; ++b) {
+                if (!s[a].written && !s[b].written) continue;
+                const Span &lo = s[a].p <= s[b].p ? s[a] : s[b], &hi = s[a].p <= s[b].p ? s[b] : s[a];
+                const int64_t gap = hi.p - lo.p;
+                if (gap >= (lo.rows - 1) * lo.pitch + lo.width) continue;
+                // column blocks of one wider matrix lie between each other's rows
+                if (lo.rows > 1 && hi.rows > 1 && lo.pitch == hi.pitch && gap % lo.pitch >= lo.width &&
+                    gap % lo.pitch + hi.width <= lo.pitch)
+                    continue;
+                c.fail(FSDPPACK_EINVAL, std::string(s[a].name) + " and " + s[b].name + " overlap in memory");
+                return true;
+            }
+        return false;
+    }
+};
+
+constexpr uint32_t kBf16 = 1u << FSDPPACK_BF16, kFp32 = 1u << FSDPPACK_FP32, kDense = kBf16 | kFp32;
+constexpr uint32_t kEight = 1u << FSDPPACK_E4M3 | 1u << FSDPPACK_INT8;
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+bool workspace_ok(Check &c, const void *ws, int64_t have, int64_t need)
+{
+    if (c.rc != FSDPPACK_OK) return false;
+    if (need > 0 && (ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 16 != 0))
+        return c.fail(FSDPPACK_EINVAL, "workspace is NULL or not aligned to 16 bytes");
+    if (have < need)
+        return c.fail(FSDPPACK_EINVAL, "workspace has " + std::to_string(have) + " bytes, " + std::to_string(need) + " are needed");
+    return true;
+}
+
+int finish(int hip_error, int launches, const char *what)
+{
+    if (hip_error != 0) return report_hip(hip_error, what);
+    count_launches(launches);
+    return FSDPPACK_OK;
+}
+
+// Every size a product's launch depends on, within the grid's limit.
+bool product_ok(Check &c, int64_t I, int64_t J, int64_t outs)
+{
+    if ((I + 31) / 32 * ((J + 15) / 16) * outs >= int64_t{1} << 31)
+        return c.fail(FSDPPACK_EINVAL, "the product needs more workgroups than a launch can hold");
+    return true;
+}
+
+int64_t partial_bytes(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
+{
+    const int splits = gemm_splits(kind, I, J, R, outs);
+    return splits > 1 ? int64_t{4} * splits * outs * I * J : 0;
+}
+
+struct GatedSpace {
+    int64_t ld, half, partial, bytes;
+};
+
+GatedSpace gated_space(int64_t rows, int64_t ffn, int64_t cols)
+{
+    GatedSpace s;
+    s.ld = round_up(ffn, 8);
+    s.half = round_up(rows * s.ld * 2, 256);
+    s.partial = std::max(partial_bytes(kGemmDx, cols, rows, ffn, 1), partial_bytes(kGemmDw, cols, ffn, rows, 2));
+    s.bytes = 2 * s.half + s.partial;
+    return s;
+}
+
+bool sizes_ok(Check &c, int64_t rows, int64_t a, int64_t b, const void *bytes)
+{
+    if (bytes == nullptr) return c.fail(FSDPPACK_EINVAL, "bytes is NULL");
+    if (rows < 0 || rows > kMaxRows || a < 1 || a > kMaxCols || b < 1 || b > kMaxCols)
+        return c.fail(FSDPPACK_EINVAL, "sizes need rows >= 0 and 1 to 2^21 columns");
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fsdppack_checkpoint_save(const fsdppack_matrix *x, const fsdppack_matrix *checkpoint, void *stream)
+try {
+    void *e0, *e1;
+    take_timing_events(&e0, &e1);
+    Check c{"checkpoint_save"};
+    Mat mx, mq;
+    if (!c.shape(x, "x") || !c.matrix(x, "x", x->rows, x->cols, kDense, &mx) ||
+        !c.matrix(checkpoint, "checkpoint", x->rows, x->cols, kEight, &mq))
+        return c.rc;
+    Spans s;
+    s.put(mx, x->rows, x->cols, false, "x");
+    s.put(mq, x->rows, x->cols, true, "checkpoint");
+    if (s.overlap(c)) return c.rc;
+    if (x->rows == 0) return FSDPPACK_OK;
+    return finish(launch_checkpoint(mx, mq, x->rows, x->cols, true, stream, e0, e1), 1, c.call);
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_checkpoint_load(const fsdppack_matrix *checkpoint, const fsdppack_matrix *out, void *stream)
+try {
+    void *e0, *e1;
+    take_timing_events(&e0, &e1);
+    Check c{"checkpoint_load"};
+    Mat mq, mo;
+    if (!c.shape(checkpoint, "checkpoint") ||
+        !c.matrix(checkpoint, "checkpoint", checkpoint->rows, checkpoint->cols, kEight, &mq) ||
+        !c.matrix(out, "out", checkpoint->rows, checkpoint->cols, kDense, &mo))
+        return c.rc;
+    Spans s;
+    s.put(mq, checkpoint->rows, checkpoint->cols, false, "checkpoint");
+    s.put(mo, checkpoint->rows, checkpoint->cols, true, "out");
+    if (s.overlap(c)) return c.rc;
+    if (checkpoint->rows == 0) return FSDPPACK_OK;
+    return finish(launch_checkpoint(mo, mq, checkpoint->rows, checkpoint->cols, false, stream, e0, e1), 1, c.call);
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_norm_forward(int32_t kind, const fsdppack_matrix *x, const void *weight, const void *bias, int32_t weight_dtype,
+                          float eps, const fsdppack_matrix *out, float *stats, const fsdppack_matrix *x_checkpoint,
+                          const fsdppack_matrix *out_checkpoint, void *stream)
+try {
+    void *e0, *e1;
+    take_timing_events(&e0, &e1);
+    Check c{"norm_forward"};
+    NormArgs a{};
+    if (kind != FSDPPACK_LAYER_NORM && kind != FSDPPACK_RMS_NORM) return c.fail(FSDPPACK_EINVAL, "unknown kind of norm"), c.rc;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return c.fail(FSDPPACK_EINVAL, "eps must be finite and not negative"), c.rc;
+    if (!c.shape(x, "x")) return c.rc;
+    const int64_t rows = x->rows, cols = x->cols;
+    if (!c.matrix(x, "x", rows, cols, kDense, &a.x) || !c.matrix(out, "out", rows, cols, kDense, &a.out) ||
+        (x_checkpoint != nullptr && !c.matrix(x_checkpoint, "x_checkpoint", rows, cols, kEight, &a.x_ckpt)) ||
+        (out_checkpoint != nullptr && !c.matrix(out_checkpoint, "out_checkpoint", rows, cols, kEight, &a.out_ckpt)) ||
+        !c.vector(weight, weight_dtype, "weight") || !c.vector(bias, weight_dtype, "bias"))
+        return c.rc;
+    if (rows > 0 && (stats == nullptr || reinterpret_cast<uintptr_t>(stats) % 4 != 0))
+        return c.fail(FSDPPACK_EINVAL, "stats is NULL or not aligned to its element size"), c.rc;
+    const int64_t wb = cols * size_of(weight_dtype);
+    Spans s;
+    s.put(a.x, rows, cols, false, "x");
+    s.put(weight, 1, wb, 0, false, "weight");
+    s.put(bias, 1, wb, 0, false, "bias");
+    s.put(a.out, rows, cols, true, "out");
+    s.put(stats, 1, rows * 8, 0, true, "stats");
+    s.put(a.x_ckpt, rows, cols, true, "x_checkpoint");
+    s.put(a.out_ckpt, rows, cols, true, "out_checkpoint");
+    if (s.overlap(c)) return c.rc;
+    if (rows == 0) return FSDPPACK_OK;
+    a.weight = weight;
+    a.bias = bias;
+    a.stats = stats;
+    a.rows = rows;
+    a.cols = static_cast<int32_t>(cols);
+    a.wdt = weight_dtype;
+    a.rms = kind == FSDPPACK_RMS_NORM;
+    a.eps = eps;
+    return finish(launch_norm_forward(a, stream, e0, e1), 1, c.call);
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_norm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes)
+try {
+    Check c{"norm_backward_workspace"};
+    if (!sizes_ok(c, rows, cols, 1, bytes)) return c.rc;
+    *bytes = int64_t{norm_backward_parts(rows, cols)} * 2 * cols * 4;
+    return FSDPPACK_OK;
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_norm_backward(int32_t kind, const fsdppack_matrix *dout, const fsdppack_matrix *x, const void *weight,
+                           int32_t weight_dtype, const float *stats, const fsdppack_matrix *dx, void *dweight, void *dbias,
+                           int32_t grad_dtype, void *workspace, int64_t workspace_bytes, void *stream)
+try {
+    void *e0, *e1;
+    take_timing_events(&e0, &e1);
+    Check c{"norm_backward"};
+    NormBackArgs a{};
+    if (kind != FSDPPACK_LAYER_NORM && kind != FSDPPACK_RMS_NORM) return c.fail(FSDPPACK_EINVAL, "unknown kind of norm"), c.rc;
+    if (!c.shape(x, "x")) return c.rc;
+    const int64_t rows = x->rows, cols = x->cols;
+    if (!c.matrix(x, "x", rows, cols, kDense | kEight, &a.x) || !c.matrix(dout, "dout", rows, cols, kDense, &a.dout) ||
+        !c.matrix(dx, "dx", rows, cols, kDense, &a.dx) || !c.vector(weight, weight_dtype, "weight") ||
+        !c.vector(dweight, grad_dtype, "dweight") || !c.vector(dbias, grad_dtype, "dbias"))
+        return c.rc;
+    if (rows > 0 && (stats == nullptr || reinterpret_cast<uintptr_t>(stats) % 4 != 0))
+        return c.fail(FSDPPACK_EINVAL, "stats is NULL or not aligned to its element size"), c.rc;
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    const int64_t need = sums ? int64_t{norm_backward_parts(rows, cols)} * 2 * cols * 4 : 0;
+    if (!workspace_ok(c, workspace, workspace_bytes, need)) return c.rc;
+    Spans s;
+    s.put(a.x, rows, cols, false, "x");
+    s.put(a.dout, rows, cols, false, "dout");
+    s.put(weight, 1, cols * size_of(weight_dtype), 0, false, "weight");
+    s.put(stats, 1, rows * 8, 0, false, "stats");
+    s.put(a.dx, rows, cols, true, "dx");
+    s.put(dweight, 1, cols * size_of(grad_dtype), 0, true, "dweight");
+    s.put(dbias, 1, cols * size_of(grad_dtype), 0, true, "dbias");
+    s.put(workspace, 1, need, 0, true, "workspace");
+    if (s.overlap(c)) return c.rc;
+    if (rows == 0 && !sums) return FSDPPACK_OK;
+    a.weight = weight;
+    a.stats = stats;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.partial = static_cast<float *>(workspace);
+    a.rows = rows;
+    a.cols = static_cast<int32_t>(cols);
+    a.wdt = weight_dtype;
+    a.gdt = grad_dtype;
+    a.rms = kind == FSDPPACK_RMS_NORM;
+    a.parts = norm_backward_parts(rows, cols);
+    int launches = 0;
+    const int e = launch_norm_backward(a, stream, e0, e1, &launches);
+    return finish(e, launches, c.call);
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features, int64_t *bytes)
+try {
+    Check c{"weight_grad_workspace"};
+    if (!sizes_ok(c, rows, out_features, in_features, bytes)) return c.rc;
+    *bytes = partial_bytes(kGemmDw, in_features, out_features, rows, 1);
+    return FSDPPACK_OK;
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_weight_grad(const fsdppack_matrix *dout, const fsdppack_matrix *x, const fsdppack_matrix *dweight,
+                         void *workspace, int64_t workspace_bytes, void *stream)
+try {
+    void *e0, *e1;
+    take_timing_events(&e0, &e1);
+    Check c{"weight_grad"};
+    GemmArgs g{};
+    if (!c.shape(x, "x") || !c.shape(dout, "dout")) return c.rc;
+    const int64_t rows = x->rows, cols = x->cols, outs = dout->cols;
+    if (!c.matrix(x, "x", rows, cols, kBf16 | kEight, &g.a[0]) || !c.matrix(dout, "dout", rows, outs, kBf16, &g.b[0]) ||
+        !c.matrix(dweight, "dweight", outs, cols, kDense, &g.out[0]) || !product_ok(c, cols, outs, 1))
+        return c.rc;
+    const int64_t need = partial_bytes(kGemmDw, cols, outs, rows, 1);
+    if (!workspace_ok(c, workspace, workspace_bytes, need)) return c.rc;
+    Spans s;
+    s.put(g.a[0], rows, cols, false, "x");
+    s.put(g.b[0], rows, outs, false, "dout");
+    s.put(g.out[0], outs, cols, true, "dweight");
+    s.put(workspace, 1, need, 0, true, "workspace");
+    if (s.overlap(c)) return c.rc;
+    g.partial = static_cast<float *>(workspace);
+    g.I = cols;
+    g.J = outs;
+    g.R = rows;
+    g.segs = 1;
+    g.outs = 1;
+    g.splits = gemm_splits(kGemmDw, cols, outs, rows, 1);
+    int launches = 0;
+    const int e = launch_gemm(kGemmDw, g, stream, e0, e1, &launches);
+    return finish(e, launches, c.call);
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_gated_forward(int32_t act, const fsdppack_matrix *x, const fsdppack_matrix *w_gate, const fsdppack_matrix *w_up,
+                           const fsdppack_matrix *out, const fsdppack_matrix *gate, const fsdppack_matrix *up, void *stream)
+try {
+    void *e0, *e1;
+    take_timing_events(&e0, &e1);
+    Check c{"gated_forward"};
+    GemmArgs g{};
+    if (act != FSDPPACK_SILU && act != FSDPPACK_GELU_TANH) return c.fail(FSDPPACK_EINVAL, "unknown activation"), c.rc;
+    if (!c.shape(x, "x") || !c.shape(out, "out")) return c.rc;
+    const int64_t rows = x->rows, cols = x->cols, ffn = out->cols;
+    if (!c.matrix(x, "x", rows, cols, kBf16, &g.b[0]) || !c.matrix(w_gate, "w_gate", ffn, cols, kBf16, &g.a[0]) ||
+        !c.matrix(w_up, "w_up", ffn, cols, kBf16, &g.a[1]) || !c.matrix(out, "out", rows, ffn, kBf16, &g.out[0]) ||
+        (gate != nullptr && !c.matrix(gate, "gate", rows, ffn, kBf16 | kEight, &g.gate)) ||
+        (up != nullptr && !c.matrix(up, "up", rows, ffn, kBf16 | kEight, &g.up)) || !product_ok(c, ffn, rows, 2))
+        return c.rc;
+    Spans s;
+    s.put(g.b[0], rows, cols, false, "x");
+    s.put(g.a[0], ffn, cols, false, "w_gate");
+    s.put(g.a[1], ffn, cols, false, "w_up");
+    s.put(g.out[0], rows, ffn, true, "out");
+    s.put(g.gate, rows, ffn, true, "gate");
+    s.put(g.up, rows, ffn, true, "up");
+    if (s.overlap(c)) return c.rc;
+    if (rows == 0) return FSDPPACK_OK;
+    g.I = ffn;
+    g.J = rows;
+    g.R = cols;
+    g.segs = 1;
+    g.outs = 1;
+    g.splits = 1;
+    g.act = act;
+    int launches = 0;
+    const int e = launch_gemm(kGemmGated, g, stream, e0, e1, &launches);
+    return finish(e, launches, c.call);
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_gated_backward_workspace(int64_t rows, int64_t ffn, int64_t cols, int64_t *bytes)
+try {
+    Check c{"gated_backward_workspace"};
+    if (!sizes_ok(c, rows, ffn, cols, bytes)) return c.rc;
+    *bytes = gated_space(rows, ffn, cols).bytes;
+    return FSDPPACK_OK;
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+int fsdppack_gated_backward(int32_t act, const fsdppack_matrix *dout, const fsdppack_matrix *x, const fsdppack_matrix *w_gate,
+                            const fsdppack_matrix *w_up, const fsdppack_matrix *gate, const fsdppack_matrix *up,
+                            const fsdppack_matrix *dx, const fsdppack_matrix *dw_gate, const fsdppack_matrix *dw_up,
+                            const fsdppack_matrix *out, void *workspace, int64_t workspace_bytes, void *stream)
+try {
+    void *e0, *e1;
+    take_timing_events(&e0, &e1);
+    Check c{"gated_backward"};
+    if (act != FSDPPACK_SILU && act != FSDPPACK_GELU_TANH) return c.fail(FSDPPACK_EINVAL, "unknown activation"), c.rc;
+    if (!c.shape(x, "x") || !c.shape(dout, "dout")) return c.rc;
+    const int64_t rows = x->rows, cols = x->cols, ffn = dout->cols;
+    GateArgs e{};
+    GemmArgs gx{}, gw{};
+    if (!c.matrix(dout, "dout", rows, ffn, kBf16, &e.dout) || !c.matrix(x, "x", rows, cols, kBf16 | kEight, &gw.a[0]) ||
+        !c.matrix(w_gate, "w_gate", ffn, cols, kBf16, &gx.a[0]) || !c.matrix(w_up, "w_up", ffn, cols, kBf16, &gx.a[1]) ||
+        !c.matrix(gate, "gate", rows, ffn, kBf16 | kEight, &e.gate) || !c.matrix(up, "up", rows, ffn, kBf16 | kEight, &e.up) ||
+        !c.matrix(dx, "dx", rows, cols, kDense, &gx.out[0]) || !c.matrix(dw_gate, "dw_gate", ffn, cols, kDense, &gw.out[0]) ||
+        !c.matrix(dw_up, "dw_up", ffn, cols, kDense, &gw.out[1]) ||
+        (out != nullptr && !c.matrix(out, "out", rows, ffn, kBf16, &e.out)) || !product_ok(c, cols, ffn, 2) ||
+        !product_ok(c, cols, rows, 1))
+        return c.rc;
+    const GatedSpace sp = gated_space(rows, ffn, cols);
+    if (!workspace_ok(c, workspace, workspace_bytes, sp.bytes)) return c.rc;
+    Spans s;
+    s.put(e.dout, rows, ffn, false, "dout");
+    s.put(gw.a[0], rows, cols, false, "x");
+    s.put(gx.a[0], ffn, cols, false, "w_gate");
+    s.put(gx.a[1], ffn, cols, false, "w_up");
+    s.put(e.gate, rows, ffn, false, "gate");
+    s.put(e.up, rows, ffn, false, "up");
+    s.put(gx.out[0], rows, cols, true, "dx");
+    s.put(gw.out[0], ffn, cols, true, "dw_gate");
+    s.put(gw.out[1], ffn, cols, true, "dw_up");
+    s.put(e.out, rows, ffn, true, "out");
+    s.put(workspace, 1, sp.bytes, 0, true, "workspace");
+    if (s.overlap(c)) return c.rc;
+    char *ws = static_cast<char *>(workspace);
+    e.dgate = reinterpret_cast<uint16_t *>(ws);
+    e.dup = reinterpret_cast<uint16_t *>(ws + sp.half);
+    e.rows = rows;
+    e.ldw = sp.ld;
+    e.cols = static_cast<int32_t>(ffn);
+    e.act = act;
+    int total = 0, n = 0;
+    if (rows > 0) {
+        if (int rc = launch_gate_backward(e, stream, e0, nullptr)) return report_hip(rc, c.call);
+        e0 = nullptr;
+        ++total;
+        gx.b[0] = Mat{e.dgate, nullptr, sp.ld, FSDPPACK_BF16};
+        gx.b[1] = Mat{e.dup, nullptr, sp.ld, FSDPPACK_BF16};
+        gx.partial = reinterpret_cast<float *>(ws + 2 * sp.half);
+        gx.I = cols;
+        gx.J = rows;
+        gx.R = ffn;
+        gx.segs = 2;
+        gx.outs = 1;
+        gx.splits = gemm_splits(kGemmDx, cols, rows, ffn, 1);
+        if (int rc = launch_gemm(kGemmDx, gx, stream, nullptr, nullptr, &n)) return report_hip(rc, c.call);
+        total += n;
+    }
+    gw.b[0] = Mat{e.dgate, nullptr, sp.ld, FSDPPACK_BF16};
+    gw.b[1] = Mat{e.dup, nullptr, sp.ld, FSDPPACK_BF16};
+    gw.partial = reinterpret_cast<float *>(ws + 2 * sp.half);
+    gw.I = cols;
+    gw.J = ffn;
+    gw.R = rows;
+    gw.segs = 1;
+    gw.outs = 2;
+    gw.splits = gemm_splits(kGemmDw, cols, ffn, rows, 2);
+    const int rc = launch_gemm(kGemmDw, gw, stream, e0, e1, &n);
+    return finish(rc, total + n, c.call);
+} catch (const std::bad_alloc &) {
+    return FSDPPACK_ENOMEM;
+}
+
+}  // extern "C"

@@ -1,0 +1,79 @@
+// fsdppack_train.h -- what the training operators' host code and kernels
+// share (internal): the norm, the 8-bit activation checkpoints, the weight
+// gradient and the gated feed-forward block.
+#pragma once
+
+#include <cstdint>
+#include <string>
+
+#include "../../include/fsdppack.h"
+
+namespace fsdppack {
+
+// Shared with the rest of the ABI (fsdppack_abi.cpp).
+int report(int code, const std::string &msg);              // set the thread's message, return the code
+int report_hip(int hip_error, const char *what);
+void take_timing_events(void **start, void **stop);        // the thread's armed events, now disarmed
+void count_launches(int64_t n);
+
+constexpr int kGroup = 32;            // columns that share a checkpoint's scale
+constexpr int kMinExponent = -110;    // smallest scale exponent: 2^-9 (e4m3's smallest step) times it is still normal
+constexpr int64_t kMaxStride = int64_t{1} << 21;   // elements between rows: a tile's offsets stay below 2^31 bytes
+
+// A matrix as a kernel sees it.
+struct Mat {
+    void *p = nullptr;
+    uint8_t *scales = nullptr;        // 8-bit formats: [rows, ceil(cols / 32)]
+    int64_t ld = 0;                   // elements between rows
+    int32_t dt = 0;
+};
+
+struct NormArgs {
+    Mat x, out, x_ckpt, out_ckpt;     // p = NULL: not wanted
+    const void *weight, *bias;        // NULL: 1 and 0
+    float *stats;                     // [rows, 2]: mean, 1 / standard deviation
+    int64_t rows;
+    int32_t cols, wdt, rms;
+    float eps;
+};
+
+struct NormBackArgs {
+    Mat dout, x, dx;
+    const void *weight;
+    const float *stats;
+    void *dweight, *dbias;
+    float *partial;                   // [parts, 2, cols] sums of dy * xh and dy
+    int64_t rows;
+    int32_t cols, wdt, gdt, rms, parts;
+};
+
+struct GateArgs {                     // elementwise part of the gated block's backward pass
+    Mat dout, gate, up, out;          // out: h recomputed (p = NULL: not wanted)
+    uint16_t *dgate, *dup;            // [rows, ldw] bf16
+    int64_t rows, ldw;
+    int32_t cols, act;
+};
+
+// out[j, i] = sum over segments s and r < R of A_s(i, r) * B_s(j, r)
+struct GemmArgs {
+    Mat a[2], b[2];                   // operands of each segment (or of each output)
+    Mat out[2];
+    Mat gate, up;                     // gated forward: the projections kept (p = NULL: not wanted)
+    float *partial;                   // split reductions: [z, split, J, I] fp32
+    int64_t I, J, R;
+    int32_t segs, outs, splits, act;
+    int32_t tiles_i, tiles_j;
+};
+
+enum GemmKind { kGemmGated, kGemmDx, kGemmDw };
+
+int launch_checkpoint(const Mat &x, const Mat &q, int64_t rows, int64_t cols, bool save, void *stream, void *e0, void *e1);
+int norm_backward_parts(int64_t rows, int64_t cols);
+int launch_norm_forward(const NormArgs &a, void *stream, void *e0, void *e1);
+int launch_norm_backward(const NormBackArgs &a, void *stream, void *e0, void *e1, int *launches);
+int launch_gate_backward(const GateArgs &a, void *stream, void *e0, void *e1);
+// Splits of the reduction a product uses, and its partial sums' bytes.
+int gemm_splits(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs);
+int launch_gemm(GemmKind kind, GemmArgs a, void *stream, void *e0, void *e1, int *launches);
+
+}  // namespace fsdppack

@@ -1,0 +1,284 @@
+"""Training operators of libfsdppack: the norm, 8-bit activation checkpoints,
+a linear layer's weight gradient and the gated feed-forward block.
+
+Like the rest of the binding this module marshals arguments and calls the C
+ABI (``include/fsdppack.h`` has each call's formulas and rules).  Matrices are
+2-D torch tensors whose rows are contiguous (``stride(1) == 1``; rows may lie
+apart) or, where an activation may be kept in 8 bits, a ``Checkpoint``.
+
+Functions (same names as the C ABI without the ``fsdppack_`` prefix):
+  checkpoint_empty(rows, cols, fmt=E4M3, device=None)  -> Checkpoint
+  checkpoint_save(x, checkpoint, stream=None)
+  checkpoint_load(checkpoint, out, stream=None)
+  norm_forward(x, weight, out, stats, bias=None, kind=LAYER_NORM, eps=1e-5,
+               x_checkpoint=None, out_checkpoint=None, stream=None)
+  norm_backward(dout, x, weight, stats, dx, dweight, workspace, dbias=None, kind=LAYER_NORM, stream=None)
+  weight_grad(dout, x, dweight, workspace, stream=None)
+  gated_forward(x, w_gate, w_up, out, gate=None, up=None, activation=SILU, stream=None)
+  gated_backward(dout, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace,
+                 activation=SILU, out=None, stream=None)
+  norm_backward_workspace / weight_grad_workspace / gated_backward_workspace(sizes) -> bytes
+
+Workspaces are contiguous uint8 tensors of at least the bytes that the
+matching ``*_workspace`` function gives (None where that is 0).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import BF16, FP32, _check, _stream, lib
+
+E4M3 = 3
+INT8 = 4
+LAYER_NORM, RMS_NORM = 0, 1
+SILU, GELU_TANH = 0, 1
+CHECKPOINT_GROUP = 32            # columns that share a scale
+
+_CODE = {torch.bfloat16: BF16, torch.float32: FP32, torch.float8_e4m3fn: E4M3, torch.int8: INT8}
+_CHECKPOINT_DTYPE = {E4M3: torch.float8_e4m3fn, INT8: torch.int8}
+
+
+class Matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Checkpoint:
+    """An activation in 8 bits: ``values`` [rows, cols] (float8_e4m3fn or
+    int8 codes) and ``scales`` [rows, ceil(cols / 32)] (uint8, exponent +
+    127), both contiguous."""
+
+    __slots__ = ("values", "scales")
+
+    def __init__(self, values: torch.Tensor, scales: torch.Tensor):
+        self.values = values
+        self.scales = scales
+
+
+def checkpoint_empty(rows: int, cols: int, fmt: int = E4M3, device=None) -> Checkpoint:
+    """Room for an activation of [rows, cols] in 8 bits (fmt: E4M3 or INT8)."""
+    if fmt not in _CHECKPOINT_DTYPE:
+        raise ValueError(f"fmt: expected E4M3 or INT8, got {fmt}")
+    device = torch.device("cuda") if device is None else device
+    return Checkpoint(torch.empty(rows, cols, dtype=_CHECKPOINT_DTYPE[fmt], device=device),
+                      torch.empty(rows, -(-cols // CHECKPOINT_GROUP), dtype=torch.uint8, device=device))
+
+
+def _device(t, what: str, dev):
+    """The tensor lives on the current GPU: that is where the launch goes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: tensor must live on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _matrix(m, what: str, dev, eight_bit: bool = False):
+    """The C descriptor of a tensor or checkpoint (None for None)."""
+    if m is None:
+        return None
+    if type(m) is Checkpoint:
+        if not eight_bit:
+            raise TypeError(f"{what}: expected a torch.Tensor, got a Checkpoint")
+        v, s = m.values, m.scales
+        _device(v, f"{what}.values", dev)
+        _device(s, f"{what}.scales", dev)
+        if v.dim() != 2 or not v.is_contiguous() or v.dtype not in (torch.float8_e4m3fn, torch.int8):
+            raise ValueError(f"{what}.values: expected a contiguous 2-D float8_e4m3fn or int8 tensor")
+        rows, cols = v.shape
+        if s.dtype is not torch.uint8 or not s.is_contiguous() or tuple(s.shape) != (rows, -(-cols // CHECKPOINT_GROUP)):
+            raise ValueError(f"{what}.scales: expected a contiguous uint8 tensor of shape "
+                             f"({rows}, {-(-cols // CHECKPOINT_GROUP)})")
+        return Matrix(v.data_ptr(), s.data_ptr(), rows, cols, cols, _CODE[v.dtype], 0)
+    _device(m, what, dev)
+    if m.dim() != 2:
+        raise ValueError(f"{what}: expected a matrix, got {m.dim()} dimensions")
+    code = _CODE.get(m.dtype, 0)
+    if code != BF16 and code != FP32:
+        raise TypeError(f"{what}: unsupported dtype {m.dtype}")
+    rows, cols = m.shape
+    step, one = m.stride()
+    if (one != 1 and cols > 1) or (rows > 1 and step < cols):
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap")
+    return Matrix(m.data_ptr(), None, rows, cols, step if rows > 1 else cols, code, 0)
+
+
+def _vector(v, what: str, n: int, dev, dtype=None):
+    """(pointer, dtype code) of a contiguous vector of n elements."""
+    if v is None:
+        return None, 0
+    _device(v, what, dev)
+    code = _CODE.get(v.dtype, 0)
+    if (code != BF16 and code != FP32) or (dtype is not None and v.dtype is not dtype):
+        raise TypeError(f"{what}: unsupported dtype {v.dtype}")
+    if v.numel() != n or not v.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements")
+    return v.data_ptr(), code
+
+
+def _stats(t, rows: int, dev):
+    p, _ = _vector(t, "stats", 2 * rows, dev, torch.float32)
+    if t is None:
+        raise TypeError("stats: expected a torch.Tensor")
+    return p
+
+
+def _workspace(t, dev):
+    if t is None:
+        return None, 0
+    _device(t, "workspace", dev)
+    if t.dtype is not torch.uint8 or not t.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor")
+    return t.data_ptr(), t.numel()
+
+
+def _ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+_L = None
+
+
+def _lib():
+    global _L
+    if _L is None:
+        L = lib()
+        vp, i32, i64, mat = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(Matrix)
+        p64 = ctypes.POINTER(i64)
+        for name, args in (
+                ("checkpoint_save", [mat, mat, vp]),
+                ("checkpoint_load", [mat, mat, vp]),
+                ("norm_forward", [i32, mat, vp, vp, i32, ctypes.c_float, mat, vp, mat, mat, vp]),
+                ("norm_backward", [i32, mat, mat, vp, i32, vp, mat, vp, vp, i32, vp, i64, vp]),
+                ("norm_backward_workspace", [i64, i64, p64]),
+                ("weight_grad", [mat, mat, mat, vp, i64, vp]),
+                ("weight_grad_workspace", [i64, i64, i64, p64]),
+                ("gated_forward", [i32, mat, mat, mat, mat, mat, mat, vp]),
+                ("gated_backward", [i32] + [mat] * 10 + [vp, i64, vp]),
+                ("gated_backward_workspace", [i64, i64, i64, p64])):
+            f = getattr(L, "fsdppack_" + name)
+            f.argtypes, f.restype = args, ctypes.c_int
+        _L = L
+    return _L
+
+
+def checkpoint_save(x, checkpoint: Checkpoint, stream=None) -> Checkpoint:
+    """Put the activation `x` (bf16 or fp32) away in 8 bits: one power-of-two
+    scale per 32 columns, values rounded to nearest even."""
+    dev = torch.cuda.current_device()
+    mx, mq = _matrix(x, "x", dev), _matrix(checkpoint, "checkpoint", dev, True)
+    _check(_lib().fsdppack_checkpoint_save(_ref(mx), _ref(mq), _stream(stream)))
+    return checkpoint
+
+
+def checkpoint_load(checkpoint: Checkpoint, out, stream=None):
+    """Read a checkpoint's values into `out` (bf16 or fp32; both hold them exactly)."""
+    dev = torch.cuda.current_device()
+    mq, mo = _matrix(checkpoint, "checkpoint", dev, True), _matrix(out, "out", dev)
+    _check(_lib().fsdppack_checkpoint_load(_ref(mq), _ref(mo), _stream(stream)))
+    return out
+
+
+def norm_forward(x, weight, out, stats, bias=None, kind: int = LAYER_NORM, eps: float = 1e-5, x_checkpoint=None,
+                 out_checkpoint=None, stream=None):
+    """LayerNorm or RMSNorm of each row of `x` into `out`; `stats` ([rows, 2]
+    fp32) receives each row's mean and 1 / standard deviation for
+    norm_backward.  `weight` and `bias` (same dtype) may be None.
+    `x_checkpoint` and `out_checkpoint` put the input and the result away in
+    8 bits in the same pass."""
+    dev = torch.cuda.current_device()
+    mx, mo = _matrix(x, "x", dev), _matrix(out, "out", dev)
+    if mx is None or mo is None:
+        raise TypeError("x and out: expected torch.Tensors")
+    pw, dw = _vector(weight, "weight", mx.cols, dev)
+    pb, db = _vector(bias, "bias", mx.cols, dev)
+    if dw and db and dw != db:
+        raise TypeError("weight and bias must have the same dtype")
+    ps = _stats(stats, mx.rows, dev)
+    qx, qo = _matrix(x_checkpoint, "x_checkpoint", dev, True), _matrix(out_checkpoint, "out_checkpoint", dev, True)
+    _check(_lib().fsdppack_norm_forward(kind, mx, pw, pb, dw or db, eps, mo, ps, _ref(qx), _ref(qo), _stream(stream)))
+    return out
+
+
+def norm_backward_workspace(rows: int, cols: int) -> int:
+    """Workspace bytes of norm_backward."""
+    n = ctypes.c_int64()
+    _check(_lib().fsdppack_norm_backward_workspace(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def norm_backward(dout, x, weight, stats, dx, dweight, workspace, dbias=None, kind: int = LAYER_NORM, stream=None):
+    """The norm's gradients: `dx`, and `dweight` and `dbias` (same dtype, the
+    one they are packed in; None when not wanted).  `x`: the forward pass's
+    input, or the checkpoint it left of it."""
+    dev = torch.cuda.current_device()
+    md, mx, mo = _matrix(dout, "dout", dev), _matrix(x, "x", dev, True), _matrix(dx, "dx", dev)
+    if md is None or mx is None or mo is None:
+        raise TypeError("dout, x and dx: expected torch.Tensors")
+    pw, dw = _vector(weight, "weight", mx.cols, dev)
+    pg, dg = _vector(dweight, "dweight", mx.cols, dev)
+    pb, db = _vector(dbias, "dbias", mx.cols, dev)
+    if dg and db and dg != db:
+        raise TypeError("dweight and dbias must have the same dtype")
+    ps = _stats(stats, mx.rows, dev)
+    ws, nbytes = _workspace(workspace, dev)
+    _check(_lib().fsdppack_norm_backward(kind, md, mx, pw, dw, ps, mo, pg, pb, dg or db, ws, nbytes, _stream(stream)))
+    return dx
+
+
+def weight_grad_workspace(rows: int, out_features: int, in_features: int) -> int:
+    """Workspace bytes of weight_grad."""
+    n = ctypes.c_int64()
+    _check(_lib().fsdppack_weight_grad_workspace(rows, out_features, in_features, ctypes.byref(n)))
+    return n.value
+
+
+def weight_grad(dout, x, dweight, workspace, stream=None):
+    """A linear layer's weight gradient dweight = dout^T x (bf16 or fp32),
+    from `dout` (bf16) and the layer's input `x` (bf16, or its checkpoint)."""
+    dev = torch.cuda.current_device()
+    md, mx, mo = _matrix(dout, "dout", dev), _matrix(x, "x", dev, True), _matrix(dweight, "dweight", dev)
+    ws, nbytes = _workspace(workspace, dev)
+    _check(_lib().fsdppack_weight_grad(_ref(md), _ref(mx), _ref(mo), ws, nbytes, _stream(stream)))
+    return dweight
+
+
+def gated_forward(x, w_gate, w_up, out, gate=None, up=None, activation: int = SILU, stream=None):
+    """The gated feed-forward block, out = act(x w_gate^T) * (x w_up^T), all
+    bf16.  `gate` and `up` (bf16 tensors or checkpoints) keep the two
+    projections for gated_backward."""
+    dev = torch.cuda.current_device()
+    mx, mg, mu, mo = (_matrix(x, "x", dev), _matrix(w_gate, "w_gate", dev), _matrix(w_up, "w_up", dev),
+                      _matrix(out, "out", dev))
+    kg, ku = _matrix(gate, "gate", dev, True), _matrix(up, "up", dev, True)
+    _check(_lib().fsdppack_gated_forward(activation, _ref(mx), _ref(mg), _ref(mu), _ref(mo), _ref(kg), _ref(ku),
+                                         _stream(stream)))
+    return out
+
+
+def gated_backward_workspace(rows: int, ffn: int, cols: int) -> int:
+    """Workspace bytes of gated_backward."""
+    n = ctypes.c_int64()
+    _check(_lib().fsdppack_gated_backward_workspace(rows, ffn, cols, ctypes.byref(n)))
+    return n.value
+
+
+def gated_backward(dout, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace, activation: int = SILU, out=None,
+                   stream=None):
+    """The gated block's gradients `dx`, `dw_gate` and `dw_up` (bf16 or fp32)
+    from `dout` (bf16), its input `x` and the projections `gate` and `up`
+    that gated_forward kept (each bf16 or a checkpoint).  `out`, if given,
+    receives the block's result again (for the weight gradient of the
+    projection behind it)."""
+    dev = torch.cuda.current_device()
+    mats = [_matrix(dout, "dout", dev), _matrix(x, "x", dev, True), _matrix(w_gate, "w_gate", dev),
+            _matrix(w_up, "w_up", dev), _matrix(gate, "gate", dev, True), _matrix(up, "up", dev, True),
+            _matrix(dx, "dx", dev), _matrix(dw_gate, "dw_gate", dev), _matrix(dw_up, "dw_up", dev),
+            _matrix(out, "out", dev)]
+    ws, nbytes = _workspace(workspace, dev)
+    _check(_lib().fsdppack_gated_backward(activation, *[_ref(m) for m in mats], ws, nbytes, _stream(stream)))
+    return dx

@@ -87,7 +87,9 @@ extern "C" {
 enum fsdppack_dtype {
     FSDPPACK_DTYPE_NONE = 0,   /* reduce_dtype only: "unset", use the grad dtype */
     FSDPPACK_BF16 = 1,
-    FSDPPACK_FP32 = 2
+    FSDPPACK_FP32 = 2,
+    FSDPPACK_E4M3 = 3,         /* matrices only: 8-bit checkpoint, float8 e4m3 codes (no infinities) */
+    FSDPPACK_INT8 = 4          /* matrices only: 8-bit checkpoint, integers -127..127 */
 };
 
 enum fsdppack_status {
@@ -285,6 +287,140 @@ int fsdppack_reduce_scatter_copy_out(const fsdppack_plan *plan, int32_t bucket, 
  * misaligned pointer), ESTATE, EHIP, ENOMEM. */
 int fsdppack_reduce_scatter_copy_out_all(const fsdppack_plan *plan, int32_t rank, const void *const *rs_outs,
                                          float divide_factor, void *const *shard_grads, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Training operators: what makes the gradients that the pack takes, for the
+ * feed-forward half of a block and its activations: the norm before it, the
+ * gated feed-forward block, a linear layer's weight gradient, and activation
+ * checkpoints in 8 bits that the backward passes read as they are.
+ *
+ * Conventions beyond those above:
+ *  - A matrix is a fsdppack_matrix: `rows` rows of `cols` elements, `stride`
+ *    elements between the starts of two rows (stride >= cols; not looked at
+ *    when rows < 2), 1 <= cols <= 2^21, stride <= 2^21, rows >= 0.  data is
+ *    aligned to its element size.  The struct is read during the call only.
+ *  - No output may share memory with another argument of the call (EINVAL);
+ *    column blocks of one wider matrix are apart and are fine.
+ *  - Workspaces are the caller's: at least the bytes that the matching
+ *    *_workspace call gives for the same sizes, aligned to 16, contents
+ *    neither read before written nor kept.  Calls that overlap on the GPU
+ *    need workspaces of their own; calls ordered on one stream may share one.
+ *  - Everything runs on `stream`, allocates nothing and waits for nothing, so
+ *    every call may be captured into a graph.  Pointers are read at the call:
+ *    a replay uses the buffers of the captured call.
+ *  - A call may launch several kernels (stated with each); timing events set
+ *    by fsdppack_time_next_launch are stamped at the start of its first and
+ *    the end of its last kernel.
+ *  - Sums, statistics and the products' accumulators are fp32; each output is
+ *    rounded to its dtype once, to nearest even.  Sums are added in an order
+ *    fixed by the sizes: the same inputs give the same bits.
+ *  - NaN and infinity go through as the formulas have it.
+ */
+
+/* A dense or 8-bit matrix.  dtype: FSDPPACK_BF16 or FSDPPACK_FP32 (scales
+ * unused), or an activation checkpoint: FSDPPACK_E4M3 or FSDPPACK_INT8, one
+ * byte an element, rows contiguous (stride = cols), and `scales` a
+ * [rows, ceil(cols / 32)] byte array: element (r, c) stands for
+ * code(r, c) * 2^(scales[r][c / 32] - 127). */
+typedef struct fsdppack_matrix {
+    void *data;
+    void *scales;
+    int64_t rows;
+    int64_t cols;
+    int64_t stride;
+    int32_t dtype;
+    int32_t reserved;
+} fsdppack_matrix;
+
+enum fsdppack_norm_kind { FSDPPACK_LAYER_NORM = 0, FSDPPACK_RMS_NORM = 1 };
+enum fsdppack_activation { FSDPPACK_SILU = 0, FSDPPACK_GELU_TANH = 1 };
+
+/* Put an activation away in 8 bits.  Each group of 32 consecutive columns of
+ * a row has one scale 2^e, e the smallest integer >= -110 with
+ * max |x| * 2^-e <= 448 (e4m3) or 127 (int8) over the group's finite
+ * elements; code = x * 2^-e rounded to nearest even.  An element that is not
+ * finite is stored as NaN (e4m3: 0x7f, also with the sign bit; int8: -128)
+ * and leaves its group's scale alone.  Since the scale is a power of two,
+ * every stored value is exact in bf16, and the error is at most half a step
+ * of the code: 2^-4 of the element (e4m3, down to 2^-6 * 2^e, 2^(e-10)
+ * below), 2^(e-1) (int8).  Values that half a step would carry past the
+ * largest fp32 keep the code below.
+ * x: dense; checkpoint: 8-bit, x's shape.  One launch.
+ * Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+int fsdppack_checkpoint_save(const fsdppack_matrix *x, const fsdppack_matrix *checkpoint, void *stream);
+
+/* Read an 8-bit checkpoint back: out (dense, the checkpoint's shape) = its
+ * values, exactly.  One launch.  Errors: as checkpoint_save. */
+int fsdppack_checkpoint_load(const fsdppack_matrix *checkpoint, const fsdppack_matrix *out, void *stream);
+
+/* The norm over the columns of each row of x:
+ *   out = (x - mean) * rstd * weight + bias,
+ *   rstd = 1 / sqrt(mean((x - mean)^2) + eps),
+ * mean the row's mean (FSDPPACK_LAYER_NORM) or 0 (FSDPPACK_RMS_NORM).
+ * x, out: dense.  weight, bias: cols elements of weight_dtype (BF16 or
+ * FP32), NULL for 1 and 0.  stats: [rows, 2] floats, mean and rstd of each
+ * row, for the backward pass.  x_checkpoint, out_checkpoint: NULL, or 8-bit
+ * matrices that receive x (as checkpoint_save) and the result (from its fp32
+ * value, before out's rounding), for norm_backward and weight_grad.  One
+ * launch (none when rows = 0).  Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+int fsdppack_norm_forward(int32_t kind, const fsdppack_matrix *x, const void *weight, const void *bias,
+                          int32_t weight_dtype, float eps, const fsdppack_matrix *out, float *stats,
+                          const fsdppack_matrix *x_checkpoint, const fsdppack_matrix *out_checkpoint, void *stream);
+
+/* The norm's gradients, with xh = (x - mean) * rstd from the forward pass's
+ * stats and m(.) a row's mean:
+ *   dx = rstd * (weight * dout - m(weight * dout) - xh * m(weight * dout * xh))
+ *        (without the middle term for FSDPPACK_RMS_NORM),
+ *   dweight = sum over rows of dout * xh,  dbias = sum over rows of dout.
+ * x: dense, or the 8-bit checkpoint that norm_forward left.  dout, dx:
+ * dense.  weight: NULL for 1.  dweight, dbias: cols elements of grad_dtype
+ * (BF16 or FP32: the dtype the gradient is packed in), NULL when not wanted;
+ * zero when rows = 0.  workspace: norm_backward_workspace bytes (none needed
+ * without dweight and dbias).  At most three launches.
+ * Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+int fsdppack_norm_backward(int32_t kind, const fsdppack_matrix *dout, const fsdppack_matrix *x, const void *weight,
+                           int32_t weight_dtype, const float *stats, const fsdppack_matrix *dx, void *dweight,
+                           void *dbias, int32_t grad_dtype, void *workspace, int64_t workspace_bytes, void *stream);
+int fsdppack_norm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes);
+
+/* A linear layer's weight gradient, dweight[o, i] = sum over rows r of
+ * dout[r, o] * x[r, i] (zero when rows = 0).  dout: bf16 [rows, outs].  x:
+ * [rows, cols], bf16 or an 8-bit checkpoint, whose values enter the product
+ * exactly.  dweight: dense [outs, cols], in the dtype its gradient is packed
+ * in.  At most two launches.  Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+int fsdppack_weight_grad(const fsdppack_matrix *dout, const fsdppack_matrix *x, const fsdppack_matrix *dweight,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+int fsdppack_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features, int64_t *bytes);
+
+/* The gated feed-forward block: g = x w_gate^T, u = x w_up^T and
+ *   out = act(g) * u,
+ * from the products' fp32 values, in one launch (none when rows = 0).
+ * x: bf16 [rows, cols]; w_gate, w_up: bf16 [ffn, cols]; out: bf16
+ * [rows, ffn].  gate, up: NULL, or [rows, ffn] matrices in bf16 or 8 bits
+ * that keep g and u for the backward pass.  act: FSDPPACK_SILU,
+ * g / (1 + e^-g), or FSDPPACK_GELU_TANH,
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.
+ * Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+int fsdppack_gated_forward(int32_t act, const fsdppack_matrix *x, const fsdppack_matrix *w_gate,
+                           const fsdppack_matrix *w_up, const fsdppack_matrix *out, const fsdppack_matrix *gate,
+                           const fsdppack_matrix *up, void *stream);
+
+/* Its gradients, from dout (bf16 [rows, ffn]) and the kept g and u:
+ *   dg = dout * u * act'(g), du = dout * act(g), both rounded to bf16,
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x.
+ * x: bf16 or an 8-bit checkpoint, [rows, cols]; gate, up: bf16 or 8-bit,
+ * [rows, ffn]; dx: dense [rows, cols]; dw_gate, dw_up: dense [ffn, cols], in
+ * the dtype their gradients are packed in (zero when rows = 0).  out: NULL,
+ * or a bf16 [rows, ffn] matrix that receives act(g) * u again, for the
+ * weight gradient of the projection behind the block.  workspace:
+ * gated_backward_workspace bytes (dg, du and partial sums).  At most five
+ * launches.  Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+int fsdppack_gated_backward(int32_t act, const fsdppack_matrix *dout, const fsdppack_matrix *x,
+                            const fsdppack_matrix *w_gate, const fsdppack_matrix *w_up, const fsdppack_matrix *gate,
+                            const fsdppack_matrix *up, const fsdppack_matrix *dx, const fsdppack_matrix *dw_gate,
+                            const fsdppack_matrix *dw_up, const fsdppack_matrix *out, void *workspace,
+                            int64_t workspace_bytes, void *stream);
+int fsdppack_gated_backward_workspace(int64_t rows, int64_t ffn, int64_t cols, int64_t *bytes);
 
 /* Free a plan and its device tables.  Synchronises the device first if the
  * plan was ever used there (no kernel may still read its tables) or the

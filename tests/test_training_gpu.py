@@ -1,0 +1,744 @@
+"""The training operators on the GPU against plain 64-bit implementations.
+
+Tolerances are bounds, not observations.  u = 2^-24 is half a step of fp32
+relative to a value; `half[dtype]` the same of an output's dtype.  A sum of n
+fp32 terms in any order is off by at most (n - 1) u sum|terms|, plus one u
+for each rounding of a term; products of bf16 or 8-bit values are exact in
+fp32.  Where small integers make every step exact, equality is asked for."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+fp = pytest.importorskip("fsdp2_mixed_dtype_amd")
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+half = {BF: 2.0 ** -8, F32: U}
+EIGHT = (fp.E4M3, fp.INT8)
+
+
+@pytest.fixture(autouse=True)
+def on_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape, dtype=BF, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def strided(t, pad):
+    """The same values with `pad` more elements between rows (poisoned)."""
+    wide = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device="cuda")
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+def workspace(n):
+    """Poisoned scratch: what is read before it is written shows."""
+    return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") if n else None
+
+
+def close(got, want, bound, what=""):
+    got, want = got.double(), want.double()
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan), what
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf], want[inf]), what
+    ok = ~(nan | inf)
+    off = (got - want).abs()[ok] - torch.as_tensor(bound, dtype=torch.float64, device="cuda").expand_as(want)[ok]
+    assert off.numel() == 0 or float(off.max()) <= 0, (what, float(off.max()), int((off > 0).sum()))
+
+
+# ------------------------------------------------------------------ 8-bit checkpoints
+
+def codes(x, fmt):
+    """(values, scale bytes) by the definition, in 64 bits."""
+    x = x.double()
+    rows, cols = x.shape
+    groups = -(-cols // 32)
+    padded = torch.zeros(rows, groups * 32, dtype=torch.float64, device="cuda")
+    padded[:, :cols] = x
+    fin = torch.isfinite(padded)
+    top = torch.where(fin, padded.abs(), 0.0).view(rows, groups, 32).amax(2)
+    limit = 448.0 if fmt == fp.E4M3 else 127.0
+    e = torch.full_like(top, -110)
+    for k in range(-110, 122):                        # the smallest exponent that fits
+        e = torch.where(top * 2.0 ** -k > limit, k + 1.0, e)
+    v = padded * torch.exp2(-e).repeat_interleave(32, 1)
+    if fmt == fp.INT8:
+        q = torch.where(e.repeat_interleave(32, 1) == 122, v.clamp(-63, 63), v).round()
+    else:
+        step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+        q = (v / step).round() * step
+        q = torch.where(e.repeat_interleave(32, 1) == 120, q.clamp(-240, 240), q)
+    q = torch.where(fin, q, float("nan"))
+    return q[:, :cols], (e + 127).to(torch.uint8)
+
+
+def stored(c):
+    """A checkpoint's codes as numbers (NaN for those that stand for it)."""
+    v = c.values.double()
+    return torch.where(v == -128, float("nan"), v) if c.values.dtype is torch.int8 else v
+
+
+def values(c):
+    return stored(c) * torch.exp2(c.scales.double() - 127).repeat_interleave(32, 1)[:, :c.values.shape[1]]
+
+
+def save(x, fmt=fp.E4M3):
+    c = fp.checkpoint_empty(*x.shape, fmt=fmt)
+    c.values.view(torch.uint8).fill_(0xAA)
+    c.scales.fill_(0xAA)
+    return fp.checkpoint_save(x, c)
+
+
+def same(got, want):
+    return torch.equal(torch.nan_to_num(got, nan=12345.0), torch.nan_to_num(want, nan=12345.0))
+
+
+@pytest.mark.parametrize("fmt", EIGHT)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (1, 31, 0), (3, 32, 5), (2, 33, 1), (7, 100, 0), (65, 513, 3), (130, 4096, 8),
+                                           (5, 20000, 0), (1000, 8, 0)])
+def test_checkpoint_save_and_load(fmt, dtype, rows, cols, pad):
+    g = gen(rows * cols)
+    x = randn(g, rows, cols, dtype=dtype) * torch.exp2(torch.randint(-40, 40, (rows, cols), generator=g, device="cuda").float()).to(dtype)
+    x = torch.where(torch.rand(rows, cols, generator=g, device="cuda") < 0.2, 0.0, x.float()).to(dtype)
+    c = save(strided(x, pad) if pad else x, fmt)
+    want, scales = codes(x, fmt)
+    assert torch.equal(c.scales, scales)
+    assert same(stored(c), want)
+    for out in (BF, F32):
+        back = strided(torch.empty(rows, cols, dtype=out, device="cuda"), pad)
+        fp.checkpoint_load(c, back)
+        assert same(back.double(), values(c))
+
+
+@pytest.mark.parametrize("fmt", EIGHT)
+def test_checkpoint_special_values(fmt):
+    top = torch.finfo(F32).max
+    inf, nan = float("inf"), float("nan")
+    rows = [[0.0] * 40, [inf] * 40, [nan, -inf, 1.5] + [0.25] * 37, [top] * 20 + [-top] * 20, [2.0 ** -149] * 40,
+            [1.0, 2.0 ** -100] * 20, [448.0] + [447.99] * 39, [127.0] + [0.5] * 39, [449.0] + [127.00001] * 39,
+            [2.0 ** -120] * 40, [-0.0, 0.0] * 20, [2.0 ** k for k in range(-20, 20)], [17.0, 18.0, 19.0, 0.5, 1.5, 2.5, 126.5, 127] * 5]
+    for dtype in (F32, BF):
+        x = torch.tensor(rows, device="cuda", dtype=F32).to(dtype)
+        c = save(x, fmt)
+        want, scales = codes(x, fmt)
+        assert torch.equal(c.scales, scales)
+        assert same(stored(c), want)
+        back = fp.checkpoint_load(c, torch.empty_like(x))
+        assert same(back.double(), values(c))
+        assert bool(torch.isfinite(back[torch.isfinite(x)]).all())
+
+
+def test_checkpoint_offsets_past_32_bits():
+    rows, cols = (1 << 21) + 3, 1056                # 2.2e9 elements
+    x = torch.zeros(rows, cols, dtype=BF, device="cuda")
+    x[-1] = torch.arange(cols, device="cuda").to(BF)
+    x[-2000] = 3.0
+    c = save(x)
+    want, scales = codes(x[-2000:], fp.E4M3)
+    assert torch.equal(c.scales[-2000:], scales) and same(stored(fp.Checkpoint(c.values[-2000:], c.scales[-2000:])), want)
+    assert not bool(c.values[:-2000].view(torch.uint8).any())
+    back = fp.checkpoint_load(c, x)
+    assert same(back[-2000:].double(), values(fp.Checkpoint(c.values[-2000:], c.scales[-2000:])))
+    del x, c, back
+    torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ the norm
+
+def norm_reference(x, w, b, kind, eps=1e-5):
+    x = x.double()
+    mean = x.mean(1, keepdim=True) if kind == fp.LAYER_NORM else torch.zeros_like(x[:, :1])
+    rstd = 1 / ((x - mean).square().mean(1, keepdim=True) + eps).sqrt()
+    y = (x - mean) * rstd
+    if w is not None:
+        y = y * w.double()
+    if b is not None:
+        y = y + b.double()
+    return y, mean, rstd
+
+
+def forward_bound(x, mean, rstd, w, b, dtype, want, cols):
+    """fp32's error of the norm's result, before and after its rounding.  The
+    mean is off by at most cols u mean|x|; each row's spread relative by
+    (cols + 8) u, and by the mean's error against the spread; elementwise
+    steps add 8 u.  Sums are in fact taken in partial sums of at most
+    cols / 64 terms and a tree of 16 joins, which n stands for."""
+    n = cols / 64 + 24
+    ax = x.double().abs()
+    dm = n * U * ax.mean(1, keepdim=True)
+    size = (ax + mean.abs()) * rstd
+    ww = 1.0 if w is None else w.double().abs()
+    bound = (dm * rstd + size * U * 8 + (want.abs() if w is None and b is None else size * 1.0) * (n * U + 2 * dm * rstd)) * ww
+    if b is not None:
+        bound = bound + 4 * U * b.double().abs()
+    return bound + half[dtype] * (want.abs() + bound)
+
+
+NORM_SIZES = [(1, 1, 0), (1, 1024, 0), (3, 7, 2), (2, 64, 0), (5, 512, 0), (9, 513, 1), (33, 1000, 0), (17, 1001, 3), (70, 2048, 0),
+              (40, 2049, 0), (33, 4096, 8), (5, 5000, 0), (7, 8192, 0), (3, 12289, 0), (2, 40000, 0), (700, 512, 0)]
+
+
+@pytest.mark.parametrize("kind", [fp.LAYER_NORM, fp.RMS_NORM])
+@pytest.mark.parametrize("rows,cols,pad", NORM_SIZES)
+@pytest.mark.parametrize("xdt,odt,wdt", [(BF, BF, F32), (F32, BF, F32), (F32, F32, BF), (BF, F32, None)])
+def test_norm_forward(kind, rows, cols, pad, xdt, odt, wdt):
+    g = gen(cols * 7 + rows)
+    x = randn(g, rows, cols, dtype=xdt) + 0.5
+    w = None if wdt is None else 1 + randn(g, cols, dtype=wdt, std=0.3)
+    b = None if wdt is None or kind == fp.RMS_NORM else randn(g, cols, dtype=wdt)
+    xs = strided(x, pad)
+    out = strided(torch.zeros(rows, cols, dtype=odt, device="cuda"), pad)
+    stats = torch.full((rows, 2), float("nan"), device="cuda")
+    kept = [fp.checkpoint_empty(rows, cols, fmt=f) for f in EIGHT]
+    fp.norm_forward(xs, w, out, stats, bias=b, kind=kind, x_checkpoint=kept[0], out_checkpoint=kept[1])
+    want, mean, rstd = norm_reference(x, w, b, kind)
+    bound = forward_bound(x, mean, rstd, w, b, odt, want, cols)
+    close(out, want, bound, "out")
+    n = cols / 64 + 24
+    close(stats[:, :1], mean, n * U * x.double().abs().mean(1, keepdim=True))
+    dm = n * U * x.double().abs().mean(1, keepdim=True) * rstd
+    close(stats[:, 1:], rstd, rstd * (n * U + 2 * dm))
+    if pad:                                          # nothing between the rows was touched
+        assert bool(torch.isnan(out.as_strided((rows - 1, pad), (cols + pad, 1), cols)).all())
+    want8, scales = codes(x, fp.E4M3)
+    assert torch.equal(kept[0].scales, scales) and same(stored(kept[0]), want8)
+    # the result's checkpoint: half a step of its own codes, and fp32's error
+    e = torch.exp2(kept[1].scales.double() - 127).repeat_interleave(32, 1)[:, :cols]
+    close(values(kept[1]), want, e * 0.5 + forward_bound(x, mean, rstd, w, b, F32, want, cols), "out_checkpoint")
+    top = torch.nn.functional.pad(want.abs(), (0, -cols % 32)).view(rows, -1, 32).amax(2)
+    e = torch.exp2(kept[1].scales.double() - 127)
+    assert bool((e * 127 >= top * (1 - 1e-3)).all()) and bool((e * 63.5 <= top * (1 + 1e-3) + 2.0 ** -100).all())
+    # the same call again, without checkpoints: the same bits
+    again, stats2 = torch.empty(rows, cols, dtype=odt, device="cuda"), torch.empty(rows, 2, device="cuda")
+    fp.norm_forward(x, w, again, stats2, bias=b, kind=kind)
+    assert torch.equal(again, out) and torch.equal(stats, stats2)
+
+
+def norm_grads(dy, x, w, stats, kind):
+    dy, x, stats = dy.double(), x.double(), stats.double()
+    xh = (x - stats[:, :1]) * stats[:, 1:]
+    wdy = dy * (1.0 if w is None else w.double())
+    c1 = wdy.mean(1, keepdim=True) if kind == fp.LAYER_NORM else 0.0
+    c2 = (wdy * xh).mean(1, keepdim=True)
+    return stats[:, 1:] * (wdy - c1 - xh * c2), (dy * xh).sum(0), dy.sum(0), xh, wdy
+
+
+@pytest.mark.parametrize("kind", [fp.LAYER_NORM, fp.RMS_NORM])
+@pytest.mark.parametrize("rows,cols,pad", NORM_SIZES + [(0, 100, 0), (3000, 64, 0), (2500, 1024, 0), (300, 6000, 0)])
+@pytest.mark.parametrize("x_kind,ddt,odt,gdt", [(BF, BF, BF, F32), (F32, BF, F32, F32), (fp.E4M3, BF, BF, F32), (fp.INT8, F32, F32, BF),
+                                                (BF, F32, BF, None)])
+def test_norm_backward(kind, rows, cols, pad, x_kind, ddt, odt, gdt):
+    g = gen(cols * 3 + rows)
+    x = randn(g, rows, cols, dtype=F32 if x_kind is F32 else BF) + 0.5
+    w = 1 + randn(g, cols, dtype=F32, std=0.3) if gdt else None
+    dy = randn(g, rows, cols, dtype=ddt)
+    _, mean, rstd = norm_reference(x, None, None, kind)
+    stats = torch.cat([mean, rstd], 1).float().contiguous()
+    arg, seen = (strided(x, pad), x) if x_kind in (BF, F32) else (None, None)
+    if arg is None:
+        arg = save(x, x_kind)
+        seen = values(arg)
+    dx = strided(torch.zeros(rows, cols, dtype=odt, device="cuda"), pad)
+    dw, db = (torch.full((cols,), float("nan"), dtype=gdt, device="cuda") if gdt else None for _ in range(2))
+    fp.norm_backward(strided(dy, pad), arg, w, stats, dx, dw, workspace(fp.norm_backward_workspace(rows, cols)), dbias=db, kind=kind)
+    want, want_w, want_b, xh, wdy = norm_grads(dy, seen, w, stats, kind)
+    # xh is off by 3 u of the larger of x and the mean; the two means by n u and their terms' own errors
+    r = stats[:, 1:].double()
+    axh = 3 * U * (seen.double().abs() + stats[:, :1].double().abs()) * r
+    n = cols / 64 + 24
+    m1 = wdy.abs().mean(1, keepdim=True) if rows else 0.0
+    m2 = (wdy.abs() * (xh.abs() + axh)).mean(1, keepdim=True)
+    d2 = n * U * m2 + (wdy.abs() * axh).mean(1, keepdim=True)
+    bound = r * (8 * U * (wdy.abs() + m1 + xh.abs() * m2) + n * U * m1 + xh.abs() * d2 + axh * m2)
+    close(dx, want, bound + half[odt] * (want.abs() + bound), "dx")
+    if pad and rows > 1:
+        assert bool(torch.isnan(dx.as_strided((rows - 1, pad), (cols + pad, 1), cols)).all())
+    if gdt:
+        ad = dy.double().abs()
+        bw = (rows + 8) * U * (ad * xh.abs()).sum(0) + (ad * axh).sum(0)
+        close(dw, want_w, bw + half[gdt] * (want_w.abs() + bw), "dweight")
+        bb = (rows + 8) * U * ad.sum(0)
+        close(db, want_b, bb + half[gdt] * (want_b.abs() + bb), "dbias")
+        again = [torch.empty_like(dw), torch.empty_like(dx)]
+        fp.norm_backward(dy, arg, w, stats, again[1], again[0], workspace(fp.norm_backward_workspace(rows, cols)), kind=kind)
+        assert torch.equal(again[0], dw) and torch.equal(again[1], dx)
+
+
+@pytest.mark.parametrize("kind", [fp.LAYER_NORM, fp.RMS_NORM])
+def test_norm_gradient_against_differences(kind):
+    """dL of L = sum(out * dout) along a direction in x, w and b at once, by
+    central differences of the 64-bit forward pass (their own error, third
+    order in h, is below 1e-7 of the terms' size)."""
+    g = gen(5)
+    rows, cols = 6, 300
+    x, dy = randn(g, rows, cols, dtype=F32), randn(g, rows, cols, dtype=F32)
+    w, b = 1 + randn(g, cols, dtype=F32, std=0.3), randn(g, cols, dtype=F32)
+    tx, tw, tb = randn(g, rows, cols, dtype=F32).double(), randn(g, cols, dtype=F32).double(), randn(g, cols, dtype=F32).double()
+    h = 1e-4
+    loss = lambda s: float((norm_reference(x.double() + s * tx, w.double() + s * tw, b.double() + s * tb, kind)[0] * dy.double()).sum())  # noqa: E731
+    out, stats = torch.empty_like(x), torch.empty(rows, 2, device="cuda")
+    fp.norm_forward(x, w, out, stats, bias=b, kind=kind)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    fp.norm_backward(dy, x, w, stats, dx, dw, workspace(fp.norm_backward_workspace(rows, cols)), dbias=db, kind=kind)
+    got = float((dx.double() * tx).sum() + (dw.double() * tw).sum() + (db.double() * tb).sum())
+    size = float((dx.double() * tx).abs().sum() + (dw.double() * tw).abs().sum() + (db.double() * tb).abs().sum())
+    assert abs(got - (loss(h) - loss(-h)) / (2 * h)) <= 1e-6 * size
+
+
+def test_norm_non_finite_rows_stay_apart():
+    x = torch.randn(8, 200, device="cuda").to(BF)
+    x[2, 5] = float("inf")
+    x[5, 199] = float("nan")
+    out, stats = torch.empty_like(x), torch.empty(8, 2, device="cuda")
+    fp.norm_forward(x, None, out, stats)
+    good = [0, 1, 3, 4, 6, 7]
+    assert bool(torch.isnan(out[2]).all()) and bool(torch.isnan(out[5]).all()) and bool(torch.isfinite(out[good]).all())
+    dx, dw = torch.empty_like(x), torch.empty(200, device="cuda")
+    fp.norm_backward(torch.ones_like(x), x, None, stats, dx, dw, workspace(fp.norm_backward_workspace(8, 200)))
+    assert bool(torch.isnan(dx[2]).all()) and bool(torch.isfinite(dx[good]).all()) and bool(torch.isnan(dw).all())
+
+
+def test_norm_constant_and_zero_rows():
+    """No spread: rstd = 1 / sqrt(eps), the result the bias alone."""
+    x = torch.zeros(3, 96, device="cuda")
+    x[1] = 7.0
+    out, stats = torch.empty_like(x), torch.empty(3, 2, device="cuda")
+    b = torch.arange(96, device="cuda").float()
+    fp.norm_forward(x, None, out, stats, bias=b, eps=0.25)
+    assert torch.equal(out, b.expand(3, 96)) and torch.equal(stats[:, 1], torch.full((3,), 2.0, device="cuda"))
+
+
+# ------------------------------------------------------------------ products
+
+def integers(g, *shape, top=2):
+    return torch.randint(-top, top + 1, shape, generator=g, device="cuda").to(BF)
+
+
+PRODUCTS = [(1, 1, 1), (1, 64, 64), (3, 5, 7), (64, 128, 128), (63, 127, 129), (65, 32, 96), (100, 130, 200), (128, 256, 256),
+            (257, 300, 520), (1000, 96, 40), (2055, 512, 264), (4100, 70, 1000), (200, 1500, 1030), (0, 40, 72), (16384, 33, 65),
+            (300, 1024, 1024)]
+
+
+@pytest.mark.parametrize("rows,outs,cols", PRODUCTS)
+@pytest.mark.parametrize("x_kind", [BF, fp.E4M3, fp.INT8])
+@pytest.mark.parametrize("gdt", [BF, F32])
+def test_weight_grad_exact(rows, outs, cols, x_kind, gdt):
+    """Small integers: every product and sum is exact in fp32 (at most
+    16384 * 2 * 4 < 2^24), so only the output's rounding is left."""
+    g = gen(rows + outs * 3 + cols * 5)
+    dy, x = integers(g, rows, outs), integers(g, rows, cols, top=4)
+    arg = x if x_kind is BF else save(x, x_kind)
+    dw = torch.full((outs, cols), float("nan"), dtype=gdt, device="cuda")
+    fp.weight_grad(dy, arg, dw, workspace(fp.weight_grad_workspace(rows, outs, cols)))
+    want = dy.double().t().contiguous() @ x.double()
+    assert torch.equal(dw, want.to(gdt))
+
+
+@pytest.mark.parametrize("x_kind", [BF, fp.E4M3, fp.INT8])
+@pytest.mark.parametrize("rows,outs,cols", [(700, 200, 264), (4099, 512, 512), (90, 70, 1001)])
+def test_weight_grad_random(rows, outs, cols, x_kind):
+    g = gen(rows)
+    dy, x = randn(g, rows, outs), randn(g, rows, cols)
+    arg = strided(x, 8) if x_kind is BF else save(x, x_kind)
+    seen = x.double() if x_kind is BF else values(arg)
+    dw = strided(torch.zeros(outs, cols, dtype=F32, device="cuda"), 4)
+    fp.weight_grad(strided(dy, 16), arg, dw, workspace(fp.weight_grad_workspace(rows, outs, cols)))
+    want = dy.double().t().contiguous() @ seen
+    close(dw, want, (rows + 1) * U * (dy.double().abs().t().contiguous() @ seen.abs()))
+    assert bool(torch.isnan(dw.as_strided((outs - 1, 4), (cols + 4, 1), cols)).all())
+
+
+def test_weight_grad_non_finite():
+    """A NaN or infinity of x reaches its own column of dW only, also from 8 bits."""
+    for fmt in (None,) + EIGHT:
+        x, dy = torch.ones(100, 72, dtype=BF, device="cuda"), torch.ones(100, 40, dtype=BF, device="cuda")
+        x[7, 3], x[99, 71] = float("nan"), float("inf")
+        dw = torch.empty(40, 72, device="cuda")
+        fp.weight_grad(dy, x if fmt is None else save(x, fmt), dw, workspace(fp.weight_grad_workspace(100, 40, 72)))
+        bad = [3, 71]
+        assert not bool(torch.isfinite(dw[:, bad]).any())
+        keep = [c for c in range(72) if c not in bad]
+        assert torch.equal(dw[:, keep], torch.full((40, 70), 100.0, device="cuda"))
+
+
+def test_weight_grad_offsets_past_32_bits():
+    rows, outs, cols = 1 << 19, 4104, 64             # dout: 2.15e9 elements
+    dy = torch.zeros(rows, outs, dtype=BF, device="cuda")
+    x = torch.zeros(rows, cols, dtype=BF, device="cuda")
+    for r, v in ((0, 1.0), (rows // 2 + 1, 2.0), (rows - 1, 3.0)):
+        dy[r] = (torch.arange(outs, device="cuda") % 5).to(BF)
+        x[r] = v
+    dw = torch.empty(outs, cols, device="cuda")
+    fp.weight_grad(dy, x, dw, workspace(fp.weight_grad_workspace(rows, outs, cols)))
+    assert torch.equal(dw, ((torch.arange(outs, device="cuda") % 5) * 6.0)[:, None].expand(outs, cols))
+    del dy, x
+    torch.cuda.empty_cache()
+
+
+def act_reference(act, g):
+    if act == fp.SILU:
+        s = torch.sigmoid(g)
+        return g * s, s * (1 + g * (1 - s))
+    k = math.sqrt(2 / math.pi)
+    t = torch.tanh(k * (g + 0.044715 * g ** 3))
+    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * k * (1 + 3 * 0.044715 * g * g)
+
+
+# fp32's error of act and act' relative to the size of their terms: e^z with
+# z off by |z| u and a few roundings, the reciprocal by 2 u; |z| <= 90 counts
+# (past it act is 0 or g).  The hardware's exp2 adds 2 u and its product with
+# log2(e) another |z| u.
+ACT = 200 * U
+
+GATED = [(1, 1, 1), (1, 64, 128), (1, 1024, 4096), (2, 40, 72), (17, 33, 65), (31, 512, 256), (33, 520, 300), (64, 64, 64), (100, 96, 40),
+         (129, 200, 520), (300, 1024, 192), (16, 4096, 100), (513, 264, 1030), (5, 1000, 2055)]
+
+
+@pytest.mark.parametrize("act", [fp.SILU, fp.GELU_TANH])
+@pytest.mark.parametrize("rows,cols,ffn", GATED)
+@pytest.mark.parametrize("keep", [None, BF, fp.E4M3, fp.INT8])
+def test_gated_forward(act, rows, cols, ffn, keep):
+    g = gen(rows + cols + ffn)
+    x = randn(g, rows, cols)
+    wg, wu = (randn(g, ffn, cols, std=2 / math.sqrt(cols)) for _ in range(2))
+    out = torch.full((rows, ffn), float("nan"), dtype=BF, device="cuda")
+    make = lambda: None if keep is None else torch.empty_like(out) if keep is BF else fp.checkpoint_empty(rows, ffn, fmt=keep)  # noqa: E731
+    gate, up = make(), make()
+    fp.gated_forward(x, wg, wu, out, gate=gate, up=up, activation=act)
+    G, Up = (x.double() @ w.double().t().contiguous() for w in (wg, wu))
+    size = [(cols + 1) * U * (x.double().abs() @ w.double().abs().t().contiguous()) for w in (wg, wu)]
+    a, da = act_reference(act, G)
+    # |act'| <= 1.13, |act| <= |g| + 0.2; second-order terms are far below the last summand
+    bound = 1.2 * size[0] * Up.abs() + (a.abs() + size[0]) * size[1] + ACT * (G.abs() + 1) * Up.abs() + 4 * U * (a * Up).abs()
+    close(out, a * Up, bound + half[BF] * ((a * Up).abs() + bound), "out")
+    for kept, want, err in ((gate, G, size[0]), (up, Up, size[1])):
+        if keep is BF:
+            close(kept, want, err + half[BF] * (want.abs() + err), "kept")
+        elif keep is not None:
+            e = torch.exp2(kept.scales.double() - 127)
+            top = torch.nn.functional.pad(want.abs(), (0, -ffn % 32)).view(rows, -1, 32).amax(2)
+            slack = torch.nn.functional.pad(err, (0, -ffn % 32)).view(rows, -1, 32).amax(2)
+            most = 448.0 if keep == fp.E4M3 else 127.0
+            assert bool((e * most >= top - slack).all()) and bool((e * most / 2 <= top + slack + 2.0 ** -100).all())
+            ee = e.repeat_interleave(32, 1)[:, :ffn]
+            step = ee * 0.5 if keep == fp.INT8 else torch.maximum((want.abs() + err) * 2.0 ** -4, ee * 2.0 ** -10)
+            close(values(kept), want, err + step, "kept in 8 bits")
+
+
+@pytest.mark.parametrize("rows,cols,ffn", GATED)
+def test_gated_projections_exact(rows, cols, ffn):
+    """Small integers: g and u are exact (at most 4096 * 2 < 2^24), so are the
+    kept ones where bf16 or the 8 bits hold them."""
+    g = gen(rows * 3 + cols + ffn)
+    x, wg, wu = integers(g, rows, cols, top=1), integers(g, ffn, cols, top=1), integers(g, ffn, cols, top=2)
+    out, gate, up = (torch.empty(rows, ffn, dtype=BF, device="cuda") for _ in range(3))
+    fp.gated_forward(x, wg, wu, out, gate=gate, up=up)
+    G, Up = (x.double() @ w.double().t().contiguous() for w in (wg, wu))
+    assert torch.equal(gate, G.to(BF)) and torch.equal(up, Up.to(BF))
+    c = [fp.checkpoint_empty(rows, ffn, fmt=f) for f in EIGHT]
+    fp.gated_forward(x, wg, wu, out, gate=c[0], up=c[1])
+    for k, want, f in ((c[0], G, fp.E4M3), (c[1], Up, fp.INT8)):
+        q, s = codes(want, f)
+        assert torch.equal(k.scales, s) and same(stored(k), q)
+
+
+def backward_reference(dy, x, wg, wu, G, Up, act):
+    a, da = act_reference(act, G)
+    dg, du = dy.double() * Up * da, dy.double() * a
+    return dg, du, a * Up
+
+
+@pytest.mark.parametrize("act", [fp.SILU, fp.GELU_TANH])
+@pytest.mark.parametrize("rows,cols,ffn", GATED + [(2055, 512, 264), (0, 40, 72)])
+@pytest.mark.parametrize("kept,x_kind,gdt", [(BF, BF, BF), (fp.E4M3, fp.E4M3, F32), (fp.INT8, BF, F32), (BF, fp.INT8, F32)])
+def test_gated_backward(act, rows, cols, ffn, kept, x_kind, gdt):
+    g = gen(rows * 2 + cols + ffn)
+    x, dy = randn(g, rows, cols), randn(g, rows, ffn)
+    wg, wu = (randn(g, ffn, cols, std=2 / math.sqrt(cols)) for _ in range(2))
+    gate, up = randn(g, rows, ffn, std=2.0), randn(g, rows, ffn)
+    ax = x if x_kind is BF else save(x, x_kind)
+    ag, au = (gate, up) if kept is BF else (save(gate, kept), save(up, kept))
+    see = lambda t: t.double() if isinstance(t, torch.Tensor) else values(t)  # noqa: E731
+    dx = torch.full((rows, cols), float("nan"), dtype=gdt, device="cuda")
+    dwg, dwu = (torch.full((ffn, cols), float("nan"), dtype=gdt, device="cuda") for _ in range(2))
+    h = torch.full((rows, ffn), float("nan"), dtype=BF, device="cuda")
+    ws = workspace(fp.gated_backward_workspace(rows, ffn, cols))
+    fp.gated_backward(dy, ax, wg, wu, ag, au, dx, dwg, dwu, ws, activation=act, out=h)
+    G, Up, X = see(ag), see(au), see(ax)
+    dg, du, hh = backward_reference(dy, x, wg, wu, G, Up, act)
+    # the terms' errors: fp32's, then half a step of bf16
+    ad = dy.double().abs()
+    eg = ACT * 4 * (G.abs() + 1) * Up.abs() * ad
+    eu = ACT * (G.abs() + 1) * ad
+    close(h, hh, (ACT * (G.abs() + 1) * Up.abs()) * 1.01 + half[BF] * hh.abs() * 1.01, "out")
+    eg, eu = eg * 1.01 + half[BF] * dg.abs() * 1.01, eu * 1.01 + half[BF] * du.abs() * 1.01
+    mm = lambda p, q: p @ q  # noqa: E731
+    want = mm(dg, wg.double()) + mm(du, wu.double())
+    bound = mm(eg, wg.double().abs()) + mm(eu, wu.double().abs())
+    bound = bound + (2 * ffn + 2) * U * (mm(dg.abs() + eg, wg.double().abs()) + mm(du.abs() + eu, wu.double().abs()))
+    close(dx, want, bound + half[gdt] * (want.abs() + bound), "dx")
+    # bounds are worst cases; the errors are random, so their norm is far smaller:
+    # half a step of bf16 in the terms and in the result
+    if want.numel() >= 10000:
+        assert float((dx.double() - want).norm() / want.norm()) <= 2.0 ** -8
+    for got, d, e in ((dwg, dg, eg), (dwu, du, eu)):
+        want = mm(d.t().contiguous(), X)
+        bound = mm(e.t().contiguous(), X.abs()) + (rows + 1) * U * mm((d.abs() + e).t().contiguous(), X.abs())
+        close(got, want, bound + half[gdt] * (want.abs() + bound), "dw")
+        if want.numel() >= 10000:
+            assert float((got.double() - want).norm()) <= 2.0 ** -8 * float(want.norm())
+    again = [torch.empty_like(t) for t in (dx, dwg, dwu)]
+    fp.gated_backward(dy, ax, wg, wu, ag, au, *again, ws, activation=act)
+    assert all(torch.equal(p, q) for p, q in zip(again, (dx, dwg, dwu)))
+
+
+@pytest.mark.parametrize("act", [fp.SILU, fp.GELU_TANH])
+def test_gated_extreme_gates(act):
+    """Gates far out: act is g or 0, its derivative 1 or 0, no NaN is made up."""
+    v = [0.0, -0.0, 100.0, -100.0, 1e4, -1e4, 3e38, -3e38, 1e-30, -20.0, 20.0, 5e18, -5e18]
+    gate = torch.tensor([v], dtype=BF, device="cuda")
+    one = torch.ones_like(gate)
+    w = torch.zeros(len(v), 8, dtype=BF, device="cuda")
+    dx, dw, du = torch.empty(1, 8, device="cuda"), torch.empty(len(v), 8, device="cuda"), torch.empty(len(v), 8, device="cuda")
+    x = torch.ones(1, 8, dtype=BF, device="cuda")
+    h = torch.empty_like(gate)
+    fp.gated_backward(one, x, w, w, gate, one, dx, dw, du, workspace(fp.gated_backward_workspace(1, len(v), 8)), activation=act, out=h)
+    a, da = act_reference(act, gate.double())
+    da = torch.where(gate.double().abs() > 1e3, (gate > 0).double(), da)
+    a = torch.where(gate.double().abs() > 1e3, torch.where(gate > 0, gate.double(), 0.0), a)
+    close(h, a, half[BF] * 1.01 * a.abs() + 1e-6)
+    close(dw[:, 0], da[0], half[BF] * 1.01 * da[0].abs() + 1e-6)
+    close(du[:, 0], a[0], half[BF] * 1.01 * a[0].abs() + 1e-6)
+
+
+def test_gated_strides():
+    """Every operand a block of columns of a wider matrix; gate and up interleaved by rows in one."""
+    g = gen(9)
+    rows, cols, ffn = 70, 96, 136
+    x, dy = strided(randn(g, rows, cols), 5), strided(randn(g, rows, ffn), 8)
+    wg, wu = strided(randn(g, ffn, cols, std=0.1), 8), strided(randn(g, ffn, cols, std=0.1), 3)
+    both = torch.empty(rows, 2 * ffn, dtype=BF, device="cuda")
+    gate, up = both[:, :ffn], both[:, ffn:]
+    out, plain = strided(torch.empty(rows, ffn, dtype=BF, device="cuda"), 1), torch.empty(rows, ffn, dtype=BF, device="cuda")
+    g2, u2 = torch.empty_like(plain), torch.empty_like(plain)
+    fp.gated_forward(x, wg, wu, out, gate=gate, up=up)
+    c = [t.contiguous() for t in (x, wg, wu, dy)]
+    fp.gated_forward(c[0], c[1], c[2], plain, gate=g2, up=u2)
+    assert torch.equal(out, plain) and torch.equal(gate, g2) and torch.equal(up, u2)
+    res = [strided(torch.empty(*s, dtype=BF, device="cuda"), 7) for s in ((rows, cols), (ffn, cols), (ffn, cols))]
+    want = [torch.empty(*s, dtype=BF, device="cuda") for s in ((rows, cols), (ffn, cols), (ffn, cols))]
+    ws = workspace(fp.gated_backward_workspace(rows, ffn, cols))
+    fp.gated_backward(dy, x, wg, wu, gate, up, *res, ws)
+    fp.gated_backward(c[3], c[0], c[1], c[2], g2, u2, *want, ws)
+    assert all(torch.equal(p, q) for p, q in zip(res, want))
+
+
+def test_gated_gradient_against_differences():
+    """dL of L = sum(out * dout) along a direction in x and both weights, by
+    central differences of the 64-bit forward pass.  The kernel's dg and du
+    are bf16 and so is the kept gate: each product term is off by less than
+    4 half steps, independently."""
+    g = gen(11)
+    rows, cols, ffn = 40, 64, 96
+    x, dy = randn(g, rows, cols), randn(g, rows, ffn)
+    wg, wu = randn(g, ffn, cols, std=0.1), randn(g, ffn, cols, std=0.1)
+    out, gate, up = (torch.empty(rows, ffn, dtype=BF, device="cuda") for _ in range(3))
+    fp.gated_forward(x, wg, wu, out, gate=gate, up=up)
+    dx, dwg, dwu = torch.empty(rows, cols, device="cuda"), torch.empty(ffn, cols, device="cuda"), torch.empty(ffn, cols, device="cuda")
+    fp.gated_backward(dy, x, wg, wu, gate, up, dx, dwg, dwu, workspace(fp.gated_backward_workspace(rows, ffn, cols)))
+    tx, tg, tu = (randn(g, *t.shape, dtype=F32).double() for t in (x, wg, wu))
+
+    def loss(s):
+        a = act_reference(fp.SILU, (x.double() + s * tx) @ (wg.double() + s * tg).t())[0]
+        return float((a * ((x.double() + s * tx) @ (wu.double() + s * tu).t()) * dy.double()).sum())
+
+    h = 1e-5
+    got = sum(float((d.double() * t).sum()) for d, t in ((dx, tx), (dwg, tg), (dwu, tu)))
+    dg, du, _ = backward_reference(dy, x, wg, wu, gate.double(), up.double(), fp.SILU)
+    terms = (dg.square() @ wg.double().square() + du.square() @ wu.double().square()).sum().sqrt()
+    terms = terms + (dg.t().square() @ x.double().square() + du.t().square() @ x.double().square()).sum().sqrt()
+    assert abs(got - (loss(h) - loss(-h)) / (2 * h)) <= 4 * 2.0 ** -8 * 3 * float(terms)
+
+
+# ------------------------------------------------------------------ together, streams, graphs
+
+def block(seed=3, rows=200, cols=264, ffn=520):
+    g = gen(seed)
+    b = dict(x=randn(g, rows, cols), w=1 + randn(g, cols, dtype=F32, std=0.2), wg=randn(g, ffn, cols, std=0.1),
+             wu=randn(g, ffn, cols, std=0.1), wd=randn(g, cols, ffn, std=0.1), dout=randn(g, rows, cols, std=0.1))
+    e = lambda *s, dtype=BF: torch.full(s, float("nan"), dtype=dtype, device="cuda")  # noqa: E731
+    b.update(y=e(rows, cols), stats=e(rows, 2, dtype=F32), h=e(rows, ffn), dy=e(rows, cols), dh=e(rows, ffn), dx=e(rows, cols),
+             h2=e(rows, ffn), dw=e(cols, dtype=F32), dwg=e(ffn, cols), dwu=e(ffn, cols), dwd=e(cols, ffn),
+             xq=fp.checkpoint_empty(rows, cols), yq=fp.checkpoint_empty(rows, cols), gq=fp.checkpoint_empty(rows, ffn),
+             uq=fp.checkpoint_empty(rows, ffn),
+             ws=workspace(max(fp.gated_backward_workspace(rows, ffn, cols), fp.norm_backward_workspace(rows, cols),
+                              fp.weight_grad_workspace(rows, cols, ffn))))
+    return b
+
+
+def step(b, stream=None):
+    """norm -> gated block -> (its output's gradient given) -> gradients -> as
+    a training step runs them; everything kept between the passes in 8 bits."""
+    kw = dict(stream=stream)
+    fp.norm_forward(b["x"], b["w"], b["y"], b["stats"], kind=fp.RMS_NORM, x_checkpoint=b["xq"], out_checkpoint=b["yq"], **kw)
+    fp.gated_forward(b["y"], b["wg"], b["wu"], b["h"], gate=b["gq"], up=b["uq"], **kw)
+    fp.gated_backward(b["dh"], b["yq"], b["wg"], b["wu"], b["gq"], b["uq"], b["dy"], b["dwg"], b["dwu"], b["ws"], out=b["h2"], **kw)
+    fp.weight_grad(b["dout"], b["h2"], b["dwd"], b["ws"], **kw)
+    fp.norm_backward(b["dy"], b["xq"], b["w"], b["stats"], b["dx"], b["dw"], b["ws"], kind=fp.RMS_NORM, **kw)
+
+
+RESULTS = ("y", "h", "h2", "dy", "dwg", "dwu", "dwd", "dx", "dw")
+
+
+def test_block_and_pack_together():
+    """A block's gradients made by the operators go into the pack; checked
+    against 64-bit formulas on what each call was given."""
+    b = block()
+    b["dh"] = (b["dout"].float() @ b["wd"].float()).to(BF)
+    step(b)
+    rows, cols = b["x"].shape
+    ffn = b["h"].shape[1]
+    X, Y, G, Up = values(b["xq"]), values(b["yq"]), values(b["gq"]), values(b["uq"])
+    y, _, _ = norm_reference(b["x"], b["w"], None, fp.RMS_NORM)
+    assert float((Y - y).norm() / y.norm()) <= 2.0 ** -4
+    dg, du, h = backward_reference(b["dh"], None, None, None, G, Up, fp.SILU)
+    rel = lambda got, want: float((got.double() - want).norm() / want.norm())  # noqa: E731
+    assert rel(b["h2"], h) <= half[BF]
+    assert rel(b["dy"], dg @ b["wg"].double() + du @ b["wu"].double()) <= 2 * half[BF]
+    assert rel(b["dwg"], dg.t().contiguous() @ Y) <= 2 * half[BF] and rel(b["dwu"], du.t().contiguous() @ Y) <= 2 * half[BF]
+    assert rel(b["dwd"], b["dout"].double().t().contiguous() @ b["h2"].double()) <= half[BF]
+    dx, dw, _, _, _ = norm_grads(b["dy"], X, b["w"], b["stats"], fp.RMS_NORM)
+    assert rel(b["dx"], dx) <= half[BF] and rel(b["dw"], dw) <= 1e-5
+    grads = [b["dwg"], b["dwu"], b["dwd"], b["dw"]]
+    plan = fp.plan_buckets([(ffn, cols, fp.BF16, fp.FP32, fp.FP32, fp.BF16)] * 2 + [(cols, ffn, fp.BF16, fp.FP32, fp.FP32, fp.BF16),
+                                                                                 (cols, 1, fp.FP32, 0, fp.FP32, fp.FP32)], 4)
+    assert len(plan.buckets) == 1
+    k = plan.buckets[0]
+    packed = fp.pack_reduce_scatter_input(plan, 0, grads, torch.empty(4 * k.S, device="cuda")).view(4, k.S)
+    for t, gr in enumerate(grads):
+        flat = torch.zeros(4 * k.P[t], device="cuda")
+        flat[:gr.numel()] = gr.float().flatten()
+        assert torch.equal(packed[:, k.O[t]:k.O[t] + k.P[t]].flatten(), flat)
+    plan.destroy()
+
+
+def test_other_streams():
+    """The stream argument and torch's current stream both carry the work."""
+    want = block()
+    want["dh"].fill_(0.01)
+    step(want)
+    torch.cuda.synchronize()
+    for explicit in (True, False):
+        b = block()
+        b["dh"].fill_(0.01)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        if explicit:
+            step(b, stream=s)
+        else:
+            with torch.cuda.stream(s):
+                step(b)
+        s.synchronize()
+        for name in RESULTS:
+            assert torch.equal(b[name], want[name]), (explicit, name)
+
+
+def test_two_streams_at_once():
+    want = [block(seed=k) for k in (1, 2)]
+    got = [block(seed=k) for k in (1, 2)]
+    for b in want + got:
+        b["dh"].fill_(0.01)
+    for b in want:
+        step(b)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in got]
+    for _ in range(5):
+        for s, b in zip(streams, got):
+            step(b, stream=s)
+    torch.cuda.synchronize()
+    for b, w in zip(got, want):
+        for name in RESULTS:
+            assert torch.equal(b[name], w[name]), name
+
+
+def test_captured_step_replays():
+    """A captured step, replayed with new inputs in the same buffers and eager
+    work between, gives the eager results every time."""
+    b = block()
+    b["dh"].fill_(0.01)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(b)
+    for k in range(4):
+        e = block(seed=20 + k)
+        e["dh"].copy_(randn(gen(k), *e["dh"].shape, std=0.1))
+        for name in ("x", "w", "wg", "wu", "dout", "dh"):
+            b[name].copy_(e[name])
+        for name in RESULTS:
+            b[name].fill_(float("nan"))
+        graph.replay()
+        step(e)
+        torch.cuda.synchronize()
+        for name in RESULTS:
+            assert torch.equal(b[name], e[name]), (k, name)
+        torch.randn(1000, device="cuda").sum().item()
+
+
+def test_timing_events_bracket_the_call():
+    b = block()
+    b["dh"].fill_(0.01)
+    start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    stop.record()
+    torch.cuda.synchronize()
+    before = fp.counters()[0]
+    fp.time_next_launch(start, stop)
+    step(b)
+    torch.cuda.synchronize()
+    assert 0 < start.elapsed_time(stop) < 100
+    assert fp.counters()[0] - before >= 5
+
+
+def test_refusals_leave_outputs_alone():
+    x = torch.zeros(4, 64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        fp.checkpoint_save(x.t(), fp.checkpoint_empty(64, 4))
+    with pytest.raises(ValueError, match="dimensions"):
+        fp.weight_grad(x[0], x, x, None)
+    with pytest.raises(TypeError, match="float16"):
+        fp.checkpoint_save(x.half(), fp.checkpoint_empty(4, 64))
+    with pytest.raises(ValueError, match="overlap"):
+        fp.checkpoint_save(x[:1].expand(4, 64), fp.checkpoint_empty(4, 64))
+    with pytest.raises(ValueError, match="scales"):
+        fp.checkpoint_load(fp.Checkpoint(torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.zeros(4, 1, dtype=torch.uint8, device="cuda")), x)
+    stats = torch.zeros(4, 2, device="cuda")
+    with pytest.raises(ValueError, match="stats"):
+        fp.norm_forward(x, None, torch.empty_like(x), stats[:2])
+    with pytest.raises(ValueError, match="weight"):
+        fp.norm_forward(x, torch.zeros(63, device="cuda"), torch.empty_like(x), stats)
+    with pytest.raises(TypeError, match="same dtype"):
+        fp.norm_forward(x, torch.zeros(64, device="cuda"), torch.empty_like(x), stats, bias=torch.zeros(64, device="cuda", dtype=BF))
+    with pytest.raises(fp.FsdpPackError, match="overlap"):
+        fp.norm_forward(x, None, x, stats)
+    with pytest.raises(fp.FsdpPackError, match="workspace"):
+        fp.norm_backward(x, x.clone(), None, stats, torch.empty_like(x), torch.empty(64, device="cuda"), None)
+    with pytest.raises(fp.FsdpPackError, match="shape"):
+        fp.gated_forward(x, torch.zeros(8, 63, dtype=BF, device="cuda"), x, torch.empty(4, 8, dtype=BF, device="cuda"))
+    assert not bool(x.any())

@@ -1,0 +1,234 @@
+"""The training operators' argument checks: the binding's on host tensors, and
+the C ABI's own (synchronous, before anything is launched), which need no GPU:
+the addresses given here are never read."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+fp = pytest.importorskip("fsdp2_mixed_dtype_amd")
+from fsdp2_mixed_dtype_amd import training  # noqa: E402
+
+BF16, FP32, E4M3, INT8 = fp.BF16, fp.FP32, fp.E4M3, fp.INT8
+OK, EINVAL, EDTYPE = 0, -1, -2
+BASE = 1 << 40
+
+
+def L():
+    return training._lib()
+
+
+class Space:
+    """Distinct made-up addresses."""
+
+    def __init__(self):
+        self.at = BASE
+
+    def take(self, nbytes):
+        p = self.at
+        self.at += (nbytes + 4095) // 4096 * 4096 + 4096
+        return p
+
+    def mat(self, rows, cols, dtype=BF16, stride=None, data=None, scales=None):
+        size = {BF16: 2, FP32: 4}.get(dtype, 1)
+        stride = cols if stride is None else stride
+        p = self.take(max(1, rows) * max(1, abs(stride)) * size) if data is None else data
+        if dtype in (E4M3, INT8) and scales is None:
+            scales = self.take(rows * ((cols + 31) // 32) + 1)
+        return training.Matrix(p, scales, rows, cols, stride, dtype, 0)
+
+
+def message():
+    return fp.lib().fsdppack_last_error().decode()
+
+
+def ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def test_host_tensors_are_rejected(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        fp.checkpoint_save(x, fp.checkpoint_empty(4, 64, device="cpu"))
+    with pytest.raises(ValueError, match="GPU"):
+        fp.norm_forward(x, None, x, torch.zeros(4, 2))
+    with pytest.raises(ValueError, match="GPU"):
+        fp.gated_forward(x, x, x, x)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        fp.weight_grad([1.0], x, x, None)
+    with pytest.raises(TypeError, match="Checkpoint"):
+        fp.weight_grad(fp.checkpoint_empty(4, 64, device="cpu"), x, x, None)
+    with pytest.raises(ValueError, match="fmt"):
+        fp.checkpoint_empty(4, 64, fmt=BF16)
+
+
+def test_checkpoint_shapes():
+    c = fp.checkpoint_empty(5, 65, fmt=INT8, device="cpu")
+    assert c.values.shape == (5, 65) and c.values.dtype is torch.int8
+    assert c.scales.shape == (5, 3) and c.scales.dtype is torch.uint8
+    assert fp.checkpoint_empty(0, 1, device="cpu").values.dtype is torch.float8_e4m3fn
+
+
+def checks():
+    """(name, call, code, message part): every way a matrix can be refused."""
+    s = Space()
+    x, q = s.mat(8, 100), s.mat(8, 100, E4M3)
+    save = lambda a, b: L().fsdppack_checkpoint_save(ref(a), ref(b), None)  # noqa: E731
+    load = lambda a, b: L().fsdppack_checkpoint_load(ref(a), ref(b), None)  # noqa: E731
+    return [
+        ("null x", lambda: save(None, q), EINVAL, "x is NULL"),
+        ("null checkpoint", lambda: save(x, None), EINVAL, "checkpoint is NULL"),
+        ("dtype of x", lambda: save(s.mat(8, 100, E4M3), q), EDTYPE, "x has an unsupported dtype"),
+        ("dtype of checkpoint", lambda: save(x, s.mat(8, 100)), EDTYPE, "unsupported dtype"),
+        ("no such dtype", lambda: save(s.mat(8, 100, 77), q), EDTYPE, "unsupported dtype"),
+        ("negative dtype", lambda: save(s.mat(8, 100, -1), q), EDTYPE, "unsupported dtype"),
+        ("shape", lambda: save(x, s.mat(8, 99, E4M3)), EINVAL, "shape"),
+        ("no columns", lambda: save(s.mat(8, 0), q), EINVAL, "columns"),
+        ("too many columns", lambda: save(s.mat(1, (1 << 21) + 1), q), EINVAL, "columns"),
+        ("negative rows", lambda: save(s.mat(-1, 100), q), EINVAL, "rows"),
+        ("short stride", lambda: save(s.mat(8, 100, stride=99), q), EINVAL, "stride"),
+        ("wide stride", lambda: save(s.mat(8, 100, stride=(1 << 21) + 1), q), EINVAL, "stride"),
+        ("strided checkpoint", lambda: save(x, s.mat(8, 100, E4M3, stride=128)), EINVAL, "contiguous"),
+        ("misaligned", lambda: save(s.mat(8, 100, data=BASE + 1), q), EINVAL, "aligned"),
+        ("misaligned fp32", lambda: save(s.mat(8, 100, FP32, data=BASE + 2), q), EINVAL, "aligned"),
+        ("no data", lambda: save(training.Matrix(None, None, 8, 100, 100, BF16, 0), q), EINVAL, "NULL"),
+        ("no scales", lambda: save(x, training.Matrix(s.take(800), None, 8, 100, 100, E4M3, 0)), EINVAL, "scales"),
+        ("overlap", lambda: save(s.mat(8, 100, data=q.data), q), EINVAL, "overlap"),
+        ("scales overlap", lambda: load(q, s.mat(8, 100, data=q.scales)), EINVAL, "overlap"),
+        ("load dtype", lambda: load(q, s.mat(8, 100, INT8)), EDTYPE, "out has an unsupported dtype"),
+    ]
+
+
+@pytest.mark.parametrize("k", range(20))
+def test_matrices_are_checked(k):
+    name, call, code, part = checks()[k]
+    assert call() == code, name
+    assert part in message(), (name, message())
+
+
+def norm_forward(kind=0, x=None, w=None, b=None, wdt=FP32, eps=1e-5, out=None, stats=None, xq=None, oq=None):
+    s = Space()
+    x = x or s.mat(8, 100)
+    out = out or s.mat(8, 100)
+    stats = s.take(64) if stats is None else stats
+    return L().fsdppack_norm_forward(kind, ref(x), w, b, wdt, eps, ref(out), stats, ref(xq), ref(oq), None)
+
+
+def test_norm_forward_is_checked():
+    s = Space()
+    far = s.take(1 << 20) + (1 << 30)
+    for kw, code, part in [
+            (dict(kind=2), EINVAL, "kind"), (dict(eps=-1.0), EINVAL, "eps"), (dict(eps=float("nan")), EINVAL, "eps"),
+            (dict(eps=float("inf")), EINVAL, "eps"), (dict(w=far, wdt=E4M3), EDTYPE, "weight"),
+            (dict(b=far, wdt=0), EDTYPE, "bias"), (dict(w=far + 2), EINVAL, "weight"), (dict(stats=0), EINVAL, "stats"),
+            (dict(stats=far + 2), EINVAL, "stats"), (dict(out=s.mat(8, 99)), EINVAL, "shape"),
+            (dict(xq=s.mat(8, 100)), EDTYPE, "x_checkpoint"), (dict(oq=s.mat(7, 100, E4M3)), EINVAL, "out_checkpoint"),
+            (dict(x=s.mat(8, 100, data=far), out=s.mat(8, 100, data=far)), EINVAL, "overlap"),
+            (dict(x=s.mat(8, 100, data=far), stats=far + 64), EINVAL, "overlap"),
+            (dict(out=s.mat(8, 100, data=far), w=far + 400), EINVAL, "overlap")]:
+        assert norm_forward(**kw) == code, kw
+        assert part in message(), (kw, message())
+
+
+def test_norm_backward_is_checked():
+    s = Space()
+    n = ctypes.c_int64()
+    assert L().fsdppack_norm_backward_workspace(8, 100, ctypes.byref(n)) == OK and n.value > 0
+
+    def call(kind=0, dout=None, x=None, w=None, stats=s.take(64), dx=None, dw=s.take(400), db=None, gdt=FP32,
+             ws=s.take(n.value), nbytes=n.value):
+        return L().fsdppack_norm_backward(kind, ref(dout or s.mat(8, 100)), ref(x or s.mat(8, 100)), w, FP32, stats,
+                                          ref(dx or s.mat(8, 100)), dw, db, gdt, ws, nbytes, None)
+
+    shared = s.take(4096)
+    for kw, code, part in [
+            (dict(kind=-1), EINVAL, "kind"), (dict(stats=0), EINVAL, "stats"), (dict(gdt=INT8), EDTYPE, "dweight"),
+            (dict(ws=0), EINVAL, "workspace"), (dict(nbytes=n.value - 1), EINVAL, "bytes"),
+            (dict(ws=s.take(n.value) + 8), EINVAL, "16"), (dict(dout=s.mat(9, 100)), EINVAL, "dout"),
+            (dict(dx=s.mat(8, 101)), EINVAL, "dx"), (dict(dx=s.mat(8, 100, INT8)), EDTYPE, "dx"),
+            (dict(dout=s.mat(8, 100, data=shared), dx=s.mat(8, 100, data=shared)), EINVAL, "overlap"),
+            (dict(dw=shared, db=shared + 396), EINVAL, "overlap")]:
+        assert call(**kw) == code, kw
+        assert part in message(), (kw, message())
+    assert L().fsdppack_norm_backward_workspace(-1, 100, ctypes.byref(n)) == EINVAL
+    assert L().fsdppack_norm_backward_workspace(1, 0, ctypes.byref(n)) == EINVAL
+    assert L().fsdppack_norm_backward_workspace(1, 1, None) == EINVAL
+
+
+def test_weight_grad_is_checked():
+    s = Space()
+
+    def call(dout=None, x=None, dw=None, ws=s.take(1 << 30), nbytes=1 << 30):
+        return L().fsdppack_weight_grad(ref(dout or s.mat(64, 48)), ref(x or s.mat(64, 100, E4M3)),
+                                        ref(dw or s.mat(48, 100)), ws, nbytes, None)
+
+    shared = s.take(1 << 16)
+    for kw, code, part in [
+            (dict(dout=s.mat(64, 48, FP32)), EDTYPE, "dout"), (dict(x=s.mat(64, 100, FP32)), EDTYPE, "x"),
+            (dict(x=s.mat(63, 100)), EINVAL, "dout"), (dict(dw=s.mat(100, 48)), EINVAL, "dweight"),
+            (dict(dw=s.mat(48, 100, E4M3)), EDTYPE, "dweight"),
+            (dict(dout=s.mat(64, 48, data=shared), dw=s.mat(48, 100, data=shared + 64)), EINVAL, "overlap")]:
+        assert call(**kw) == code, kw
+        assert part in message(), (kw, message())
+
+
+def test_gated_calls_are_checked():
+    s = Space()
+    R, K, F = 16, 40, 24
+    n = ctypes.c_int64()
+    assert L().fsdppack_gated_backward_workspace(R, F, K, ctypes.byref(n)) == OK and n.value >= 2 * 2 * R * F
+
+    def forward(act=0, x=None, wg=None, wu=None, out=None, gate=None, up=None):
+        return L().fsdppack_gated_forward(act, ref(x or s.mat(R, K)), ref(wg or s.mat(F, K)), ref(wu or s.mat(F, K)),
+                                          ref(out or s.mat(R, F)), ref(gate), ref(up), None)
+
+    shared = s.take(1 << 16)
+    for kw, code, part in [
+            (dict(act=2), EINVAL, "activation"), (dict(x=s.mat(R, K, FP32)), EDTYPE, "x"),
+            (dict(x=s.mat(R, K, E4M3)), EDTYPE, "x"), (dict(wg=s.mat(F, K + 1)), EINVAL, "w_gate"),
+            (dict(wu=s.mat(F - 1, K)), EINVAL, "w_up"), (dict(gate=s.mat(R, F, FP32)), EDTYPE, "gate"),
+            (dict(up=s.mat(R + 1, F)), EINVAL, "up"),
+            (dict(out=s.mat(R, F, data=shared), gate=s.mat(R, F, data=shared)), EINVAL, "overlap"),
+            # blocks of columns that run into each other
+            (dict(gate=s.mat(R, F, stride=2 * F, data=shared), up=s.mat(R, F, stride=2 * F, data=shared + 2 * F - 2)), EINVAL,
+             "overlap")]:
+        assert forward(**kw) == code, kw
+        assert part in message(), (kw, message())
+
+    def backward(act=0, dout=None, x=None, gate=None, up=None, dx=None, dg=None, du=None, out=None, ws=s.take(n.value),
+                 nbytes=n.value):
+        return L().fsdppack_gated_backward(act, ref(dout or s.mat(R, F)), ref(x or s.mat(R, K)), ref(s.mat(F, K)),
+                                           ref(s.mat(F, K)), ref(gate or s.mat(R, F)), ref(up or s.mat(R, F, INT8)),
+                                           ref(dx or s.mat(R, K)), ref(dg or s.mat(F, K)), ref(du or s.mat(F, K)), ref(out),
+                                           ws, nbytes, None)
+
+    for kw, code, part in [
+            (dict(act=-1), EINVAL, "activation"), (dict(dout=s.mat(R, F, FP32)), EDTYPE, "dout"),
+            (dict(gate=s.mat(R, F, FP32)), EDTYPE, "gate"), (dict(dx=s.mat(R, K, E4M3)), EDTYPE, "dx"),
+            (dict(dg=s.mat(K, F)), EINVAL, "dw_gate"), (dict(out=s.mat(R, F, FP32)), EDTYPE, "out"),
+            (dict(ws=0), EINVAL, "workspace"), (dict(nbytes=n.value - 1), EINVAL, "bytes"),
+            (dict(dg=s.mat(F, K, data=shared), du=s.mat(F, K, data=shared)), EINVAL, "overlap"),
+            (dict(gate=s.mat(R, F, data=shared), out=s.mat(R, F, data=shared)), EINVAL, "overlap")]:
+        assert backward(**kw) == code, kw
+        assert part in message(), (kw, message())
+
+
+def test_nothing_to_do_launches_nothing():
+    s = Space()
+    before = fp.counters()[0]
+    assert L().fsdppack_checkpoint_save(ref(s.mat(0, 100)), ref(s.mat(0, 100, INT8)), None) == OK
+    assert L().fsdppack_checkpoint_load(ref(s.mat(0, 100, INT8)), ref(s.mat(0, 100)), None) == OK
+    assert norm_forward(x=s.mat(0, 100), out=s.mat(0, 100)) == OK
+    assert L().fsdppack_gated_forward(0, ref(s.mat(0, 40)), ref(s.mat(24, 40)), ref(s.mat(24, 40)), ref(s.mat(0, 24)), None, None,
+                                      None) == OK
+    assert fp.counters()[0] == before
+
+
+def test_workspaces_grow_with_sizes_only():
+    for f, sizes in ((fp.norm_backward_workspace, (4096, 1024)), (fp.weight_grad_workspace, (2055, 2048, 512)),
+                     (fp.gated_backward_workspace, (2055, 2048, 512))):
+        assert f(*sizes) == f(*sizes) >= 0
+    assert fp.gated_backward_workspace(0, 1, 1) >= 0
+    with pytest.raises(fp.FsdpPackError, match="rows >= 0"):
+        fp.gated_backward_workspace(-1, 1, 1)
