@@ -29,217 +29,383 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int BK = 64;               // reduction elements per step
-
-template <int DT>
-__device__ __forceinline__ u32x4 load_chunk(const Mat &m, int64_t row, int64_t col, int64_t cols)
-{
-    // 8 elements [col, col + 8) of a row as bf16 (exact), zeros past `cols`
-    u32x4 o = {0, 0, 0, 0};
-    if constexpr (DT == FSDPPACK_BF16) {
-        const uint16_t *p = static_cast<const uint16_t *>(m.p) + row * m.ld + col;
-        if (col + 8 <= cols) {
-            const u32x4u w = *reinterpret_cast<const u32x4u *>(p);
-            o = u32x4{w.x, w.y, w.z, w.w};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < cols) o[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
-        }
-    } else {
-        float v[8];
-        load8<DT>(static_cast<const char *>(m.p) + row * m.ld, m.scales + row * ((cols + kGroup - 1) / kGroup),
-                  static_cast<int32_t>(col), static_cast<int32_t>(cols), v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    }
-    return o;
-}
+constexpr int kXcds = 8;             // workgroups go round-robin over 8 dies, each with its own L2
 
 // Where a chunk of 8 elements lies in a tile's LDS image (in elements).
 //  reduction contiguous: [T][64], 8 chunks a row, chunk c at c ^ (row & 7)
 //  reduction strided:    [64][T], T / 8 chunks a row, chunk c at c ^ 4 (row & 3)
+// so that the 16-byte reads of 8 rows, and the 64-byte pieces of 4 rows that a
+// transposing read takes at once, fall into different banks.
 template <bool TR, int T>
-__device__ __forceinline__ int lds_at(int row, int chunk)
+__device__ __forceinline__ int swizzled(int row, int chunk)
 {
-    if constexpr (TR) return row * T + ((chunk ^ ((row & 3) << 2)) << 3);
-    else return row * BK + ((chunk ^ (row & 7)) << 3);
+    return TR ? chunk ^ ((row & 3) << 2) : chunk ^ (row & 7);
 }
 
-// The 8 reduction elements [16 s + 8 h, ...) of tile row / column `at + lane % 32`, h = lane / 32.
+// One operand's tile of T x 64 elements, brought into LDS by THREADS threads.
+//  DMA: 16-byte chunks straight from memory to LDS (each wavefront fills 1 KiB
+//       in order, so the swizzle is applied to the addresses that are read);
+//       chunks outside the matrix are read at an offset past the buffer's end,
+//       which gives zeros.  Needs 16-byte aligned rows of whole chunks.
+//  otherwise: through registers, any alignment and width, 8-bit codes to bf16
+//       (exact) on the way.
+// TWO: the lower half of the tile's rows is from one matrix, the upper half the
+// same rows of another.
+template <bool TR, int T, int THREADS, int DT, bool DMA, bool TWO>
+struct Loader {
+    static constexpr int kPerRow = TR ? T : BK;                 // elements of an LDS row
+    static constexpr int kUnit = DT == FSDPPACK_BF16 ? 8 : 16;  // elements per thread and load
+    static constexpr int kUnits = T * BK / kUnit / THREADS;
+    static_assert(T * BK % (kUnit * THREADS) == 0, "whole units per thread");
+    static constexpr int kRows = THREADS * kUnit / kPerRow;     // LDS rows apart: a thread's units
+    static_assert(!TWO || T / 2 % kRows == 0, "a load's rows lie in one half");
+    static constexpr uint32_t kOutside = 0x80000000u;
+
+    // 8-bit: 16 codes and their group's scale; bf16: 8 elements
+    u32x4 reg[DMA ? 1 : kUnits];
+    uint32_t scale[DT == FSDPPACK_BF16 ? 1 : kUnits];
+
+    // Start reading the tile whose first reduction element is r0 and whose
+    // first row (column, TR) is t0; R and W bound the two.
+    __device__ __forceinline__ void start(const Mat &m, const Mat &m2, int64_t t0, int64_t r0, int64_t W, int64_t R, uint16_t *lds)
+    {
+        const int tid = threadIdx.x;
+        const int row0 = tid * kUnit / kPerRow, col0 = tid * kUnit % kPerRow;
+        if constexpr (DMA) {
+            const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+            const int64_t first = TR ? r0 * m.ld + t0 : t0 * m.ld + r0;
+            auto rsrc = [&](const Mat &x) {
+                return __builtin_amdgcn_make_buffer_rsrc(static_cast<uint16_t *>(x.p) + first, 0, 0x7fffffff, 0x00020000);
+            };
+            const auto b0 = rsrc(m);
+            const auto b1 = rsrc(m2);
+            const int32_t ld = static_cast<int32_t>(m.ld);
+            const int32_t nt = static_cast<int32_t>(W - t0 < T ? W - t0 : T), nr = static_cast<int32_t>(R - r0 < BK ? R - r0 : BK);
+#pragma unroll
+            for (int c = 0; c < kUnits; ++c) {
+                const int row = row0 + c * kRows;
+                const int col = swizzled<TR, T>(row, col0 >> 3) << 3;
+                const int r = TWO ? row & (T / 2 - 1) : row;
+                const bool in = TR ? r < nr && col < nt : r < nt && col < nr;
+                const uint32_t off = in ? static_cast<uint32_t>(r * ld + col) * 2u : kOutside;
+                auto *to = (__attribute__((address_space(3))) void *)(lds + (wave * 64 + c * THREADS) * 8);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(TWO && c * kRows >= T / 2 ? b1 : b0, to, 16, off, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < kUnits; ++c) {
+                const int row = row0 + c * kRows;
+                const Mat &x = TWO && c * kRows >= T / 2 ? m2 : m;
+                const int r = TWO ? row & (T / 2 - 1) : row;
+                const int64_t mr = TR ? r0 + r : t0 + r, mc = (TR ? t0 : r0) + col0;
+                const int64_t rows = TR ? R : W, cols = TR ? W : R;
+                reg[c] = u32x4{0, 0, 0, 0};
+                if constexpr (DT != FSDPPACK_BF16) scale[c] = 0;
+                if (mr < rows && mc < cols) {
+                    if constexpr (DT == FSDPPACK_BF16) {
+                        const uint16_t *p = static_cast<const uint16_t *>(x.p) + mr * x.ld + mc;
+                        if (mc + 8 <= cols) {
+                            const u32x4u w = *reinterpret_cast<const u32x4u *>(p);
+                            reg[c] = u32x4{w.x, w.y, w.z, w.w};
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (mc + i < cols) reg[c][i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+                        }
+                    } else {
+                        const uint8_t *p = static_cast<const uint8_t *>(x.p) + mr * x.ld + mc;
+                        if (mc + 16 <= cols) {
+                            typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
+                            const u32x4b w = *reinterpret_cast<const u32x4b *>(p);
+                            reg[c] = u32x4{w.x, w.y, w.z, w.w};
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (mc + i < cols) reg[c][i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+                        }
+                        scale[c] = x.scales[mr * ((cols + kGroup - 1) / kGroup) + mc / kGroup];
+                    }
+                }
+            }
+        }
+    }
+
+    // Write the registers' tile to LDS.
+    __device__ __forceinline__ void put(uint16_t *lds)
+    {
+        if constexpr (!DMA) {
+            const int tid = threadIdx.x;
+            const int row0 = tid * kUnit / kPerRow, col0 = tid * kUnit % kPerRow;
+#pragma unroll
+            for (int c = 0; c < kUnits; ++c) {
+                const int row = row0 + c * kRows;
+#pragma unroll
+                for (int h = 0; h < kUnit / 8; ++h) {
+                    u32x4 o = reg[c];
+                    if constexpr (DT != FSDPPACK_BF16) {
+                        float v[8];
+                        decode8<DT>(reg[c][2 * h], reg[c][2 * h + 1], scale_of(static_cast<uint8_t>(scale[c])), v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                    }
+                    *reinterpret_cast<u32x4 *>(lds + row * kPerRow + (swizzled<TR, T>(row, (col0 >> 3) + h) << 3)) = o;
+                }
+            }
+        }
+    }
+};
+
+// The fragment of a piece of 32 rows (columns, TR) of a tile, from row `at`:
+// the 8 reduction elements 16 s + 8 (lane / 32) of row lane % 32.  The
+// address is one sum, so that the compiler still sees which image a read is
+// from and does not make it wait for the loads that fill the other one.
 template <bool TR, int T>
-__device__ __forceinline__ bf16x8 fragment(uint16_t *tile, int at, int s)
+__device__ __forceinline__ bf16x8 fragment(const uint16_t *tile, int at, int s)
 {
     const int lane = threadIdx.x & 63;
     if constexpr (TR) {
         // a group of 16 lanes reads 4 rows of 16 columns (lane: row lane / 4,
         // 4 columns) and gets them turned: lane = column, 4 rows
         const int g = lane >> 4, l = lane & 15;
-        const int row = 16 * s + 8 * (g >> 1) + (l >> 2), col = at + 16 * (g & 1) + 4 * (l & 3);
+        const int row = 8 * (g >> 1) + (l >> 2), col = at + 16 * (g & 1) + 4 * (l & 3);
+        const int off = row * T + (swizzled<true, T>(row, col >> 3) << 3) + (col & 7) + 16 * s * T;
         typedef bf16x4 __attribute__((address_space(3))) * lds4;
-        const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4)(tile + lds_at<true, T>(row, col >> 3) + (col & 7)));
-        const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4)(tile + lds_at<true, T>(row + 4, col >> 3) + (col & 7)));
+        const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4)(tile + off));
+        const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4)(tile + (off + 4 * T)));
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-        const int row = at + (lane & 31);
-        return *reinterpret_cast<bf16x8 *>(tile + lds_at<false, T>(row, 2 * s + (lane >> 5)));
+        const int row = lane & 31;
+        return *reinterpret_cast<const bf16x8 *>(tile + ((at + row) * BK + (swizzled<false, T>(row, 2 * s + (lane >> 5)) << 3)));
     }
 }
 
-// One 128 x 128 output tile per block of four wavefronts, 64 x 64 each.
-constexpr int T = 128, kBlockThreads = 256, kChunks = T * BK / 8 / kBlockThreads;
-
-template <GemmKind KIND, int ADT>
-__global__ void __launch_bounds__(kBlockThreads) gemm_kernel(GemmArgs g)
+// Two packed quads per lane (columns 8 q + 4 h + 0..3 of q = 0 and 1, h =
+// lane / 32) -> eight consecutive columns per lane: those of q = h.
+__device__ __forceinline__ u32x4 join_halves(u32x2 q0, u32x2 q1)
 {
-    constexpr bool ATR = KIND != kGemmGated, BTR = KIND == kGemmDw;
-    __shared__ __align__(16) uint16_t sa[2][T * BK], sb[2][T * BK];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int64_t b = blockIdx.x;
-    const int ti = static_cast<int>(b % g.tiles_i);
-    b /= g.tiles_i;
-    const int tj = static_cast<int>(b % g.tiles_j);
-    b /= g.tiles_j;
-    const int split = static_cast<int>(b % g.splits), z = static_cast<int>(b / g.splits);
-    // the gated product's tile holds 64 rows of W_gate and the same 64 of W_up
-    const int64_t i0 = int64_t{ti} * (KIND == kGemmGated ? T / 2 : T), j0 = int64_t{tj} * T;
-    const int64_t steps1 = (g.R + BK - 1) / BK, steps = steps1 * g.segs;
-    const int64_t s0 = steps * split / g.splits, s1 = steps * (split + 1) / g.splits;
+    const auto x = __builtin_amdgcn_permlane32_swap(q0.x, q1.x, false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(q0.y, q1.y, false, false);
+    return u32x4{x[0], y[0], x[1], y[1]};
+}
 
-    u32x4 ra[kChunks], rb[kChunks];
-    auto fetch = [&](int64_t step) {
+// A piece's row (32 columns from `col`, 16 per lane as the matrix cores leave
+// them) as bf16.  Both halves of the wavefront call it.
+__device__ __forceinline__ void store_row(uint16_t *row, int64_t col, int64_t cols, bool row_ok, const float *v)
+{
+    const int h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const float *q = v + 8 * p;
+        const u32x4 w = join_halves(u32x2{pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3])},
+                                    u32x2{pack_bf16(q[4], q[5]), pack_bf16(q[6], q[7])});
+        const int64_t c = col + 16 * p + 8 * h;
+        if (!row_ok) continue;
+        if (c + 8 <= cols) {
+            *reinterpret_cast<u32x4u *>(row + c) = u32x4u{w.x, w.y, w.z, w.w};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < cols) row[c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
+__device__ __forceinline__ void store_row_fp32(float *row, int64_t col, int64_t cols, bool row_ok, const float *v)
+{
+    const int h = (threadIdx.x >> 5) & 1;
+    if (!row_ok) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int64_t c = col + 8 * q + 4 * h;
+        if (c + 4 <= cols) {
+            *reinterpret_cast<f32x4u *>(row + c) = f32x4u{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + i < cols) row[c + i] = v[4 * q + i];
+        }
+    }
+}
+
+// A projection's piece kept for the backward pass.  In 8 bits, lanes l and
+// l + 32 hold one scale group (32 columns of a row) between them.
+template <int DT>
+__device__ __forceinline__ void keep_row8(const Mat &o, int64_t j, int64_t col, int64_t cols, bool row_ok, const float *v)
+{
+    const int h = (threadIdx.x >> 5) & 1;
+    float top = fmaxf(top_of8(v), top_of8(v + 8));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const int e = scale_exponent<DT>(top);
+    uint32_t w[4];
+    encode8<DT>(v, e, w[0], w[1]);
+    encode8<DT>(v + 8, e, w[2], w[3]);
+    // dword q: columns 8 q + 4 h; lanes below 32 get columns 0..15, the others 16..31
+    const u32x4 b = join_halves(u32x2{w[0], w[1]}, u32x2{w[2], w[3]});
+    if (!row_ok) return;
+    uint8_t *p = static_cast<uint8_t *>(o.p) + j * o.ld;
+    const int64_t c = col + 16 * h;
+    // b = own q0, q1 of the lower lane, then of the upper: columns 0-3, 8-11, 4-7, 12-15
+    const uint32_t d[4] = {b.x, b.z, b.y, b.w};
+    if (c + 16 <= cols) {
+        typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
+        *reinterpret_cast<u32x4b *>(p + c) = u32x4b{d[0], d[1], d[2], d[3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c + i < cols) p[c + i] = static_cast<uint8_t>(d[i >> 2] >> (8 * (i & 3)));
+    }
+    if (h == 0 && col < cols) o.scales[j * ((cols + kGroup - 1) / kGroup) + col / kGroup] = static_cast<uint8_t>(e + 127);
+}
+
+__device__ __forceinline__ void keep_row(const Mat &o, int64_t j, int64_t col, int64_t cols, bool row_ok, const float *v)
+{
+    if (o.p == nullptr) return;
+    if (o.dt == FSDPPACK_BF16) store_row(static_cast<uint16_t *>(o.p) + j * o.ld, col, cols, row_ok, v);
+    else if (o.dt == FSDPPACK_E4M3) keep_row8<FSDPPACK_E4M3>(o, j, col, cols, row_ok, v);
+    else keep_row8<FSDPPACK_INT8>(o, j, col, cols, row_ok, v);
+}
+
+// One TI x TJ output tile per block of WI x WJ wavefronts.
+//
+// Two LDS images of each operand's step; while one is multiplied the next
+// step's is brought into the other.  The last of a step's four slices is
+// multiplied after the barrier that frees its image, with the next step's
+// first fragments and the loads of the step after it already under way, so
+// that neither the barrier nor LDS nor memory latency leaves the matrix cores
+// idle.
+template <GemmKind KIND, int ADT, bool DMA_A, bool DMA_B, int TI, int TJ, int WI, int WJ>
+__global__ void __launch_bounds__(64 * WI * WJ, TI == 256 ? 2 : 2) gemm_kernel(GemmArgs g)
+{
+#if defined(__HIP_DEVICE_COMPILE__)      // the body uses device builtins that the host's pass does not know
+    constexpr bool ATR = KIND != kGemmGated, BTR = KIND == kGemmDw;
+    constexpr int THREADS = 64 * WI * WJ, NA = TI / WI / 32, NB = TJ / WJ / 32;
+    __shared__ __align__(1024) uint16_t sa0[TI * BK], sb0[TJ * BK], sa1[TI * BK], sb1[TJ * BK];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // each die takes a contiguous run of tiles, in bands of 8 tile rows of
+    // the output, so that its neighbours' operands meet in its L2
+    const int64_t per_z = int64_t{g.tiles_i} * g.tiles_j, tiles = per_z * g.splits * g.outs;
+    const int64_t run = (tiles + kXcds - 1) / kXcds;
+    int64_t t = blockIdx.x % kXcds * run + blockIdx.x / kXcds;
+    if (blockIdx.x / kXcds >= run || t >= tiles) return;
+    const int zs = static_cast<int>(t / per_z), z = zs / g.splits, split = zs % g.splits;
+    t -= zs * per_z;
+    constexpr int kBand = 8;
+    const int64_t band = t / (int64_t{kBand} * g.tiles_i);
+    const int high = static_cast<int>(g.tiles_j - band * kBand < kBand ? g.tiles_j - band * kBand : kBand);
+    const int in_band = static_cast<int>(t - band * kBand * g.tiles_i);
+    const int64_t tj = band * kBand + in_band % high, ti = in_band / high;
+    // the gated product's tile holds TI / 2 rows of W_gate and the same of W_up
+    const int64_t i0 = ti * (KIND == kGemmGated ? TI / 2 : TI), j0 = tj * TJ;
+    const int64_t i_end = KIND == kGemmGated ? (g.I < i0 + TI / 2 ? g.I : i0 + TI / 2) : g.I;
+    const int64_t steps1 = (g.R + BK - 1) / BK, steps = steps1 * g.segs;
+    const int64_t s0 = steps * split / g.splits, n = steps * (split + 1) / g.splits - s0;
+
+    Loader<ATR, TI, THREADS, ADT, DMA_A, KIND == kGemmGated> la;
+    Loader<BTR, TJ, THREADS, FSDPPACK_BF16, DMA_B, false> lb;
+    auto start = [&](int64_t k, uint16_t *sa, uint16_t *sb) {
+        const int64_t step = s0 + k;
         const int seg = step >= steps1;
         const int64_t r0 = (step - seg * steps1) * BK;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int u = tid + c * kBlockThreads;
-            if constexpr (ATR) {
-                const int64_t row = r0 + u / (T / 8), col = i0 + u % (T / 8) * 8;
-                ra[c] = row < g.R && col < g.I ? load_chunk<ADT>(g.a[seg], row, col, g.I) : u32x4{0, 0, 0, 0};
-            } else {
-                const int t = u / 8;
-                const int64_t row = i0 + (t & (T / 2 - 1)), col = r0 + u % 8 * 8;
-                ra[c] = row < g.I && col < g.R ? load_chunk<ADT>(g.a[t / (T / 2)], row, col, g.R) : u32x4{0, 0, 0, 0};
-            }
-            const Mat &mb = g.b[KIND == kGemmDw ? z : seg];
-            if constexpr (BTR) {
-                const int64_t row = r0 + u / (T / 8), col = j0 + u % (T / 8) * 8;
-                rb[c] = row < g.R && col < g.J ? load_chunk<FSDPPACK_BF16>(mb, row, col, g.J) : u32x4{0, 0, 0, 0};
-            } else {
-                const int64_t row = j0 + u / 8, col = r0 + u % 8 * 8;
-                rb[c] = row < g.J && col < g.R ? load_chunk<FSDPPACK_BF16>(mb, row, col, g.R) : u32x4{0, 0, 0, 0};
-            }
-        }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int u = tid + c * kBlockThreads;
-            constexpr int ca = ATR ? T / 8 : 8, cb = BTR ? T / 8 : 8;
-            *reinterpret_cast<u32x4 *>(&sa[buf][lds_at<ATR, T>(u / ca, u % ca)]) = ra[c];
-            *reinterpret_cast<u32x4 *>(&sb[buf][lds_at<BTR, T>(u / cb, u % cb)]) = rb[c];
-        }
+        la.start(g.a[seg], KIND == kGemmGated ? g.a[1] : g.a[seg], i0, r0, i_end, g.R, sa);
+        const Mat &b = g.b[KIND == kGemmDw ? z : seg];
+        lb.start(b, b, j0, r0, g.J, g.R, sb);
     };
 
-    const int wi = wave & 1, wj = wave >> 1;
-    // the wavefront's two 32-row pieces of A: of the gated product one of each matrix
-    const int ia[2] = {KIND == kGemmGated ? wi * 32 : wi * 64, KIND == kGemmGated ? T / 2 + wi * 32 : wi * 64 + 32};
-    f32x16 acc[2][2] = {};
-    if (s0 < s1) {
-        fetch(s0);
-        put(0);
-    }
-    for (int64_t s = s0; s < s1; ++s) {
-        const int buf = static_cast<int>(s - s0) & 1;
-        __syncthreads();
-        if (s + 1 < s1) fetch(s + 1);
+    const int wi = wave % WI, wj = wave / WI;
+    auto piece_a = [&](int m) {          // first tile row of the wavefront's piece m of A
+        if (KIND == kGemmGated) return m < NA / 2 ? wi * (TI / 2 / WI) + 32 * m : TI / 2 + wi * (TI / 2 / WI) + 32 * (m - NA / 2);
+        return wi * (TI / WI) + 32 * m;
+    };
+    auto piece_b = [&](int m) { return wj * (TJ / WJ) + 32 * m; };
+
+    f32x16 acc[NA][NB] = {};
+    bf16x8 fa[2][NA], fb[2][NB];
+    auto read = [&](int to, const uint16_t *sa, const uint16_t *sb, int s) {
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k) {
-            bf16x8 fa[2], fb[2];
+        for (int m = 0; m < NA; ++m) fa[to][m] = fragment<ATR, TI>(sa, piece_a(m), s);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                fa[n] = fragment<ATR, T>(sa[buf], ia[n], k);
-                fb[n] = fragment<BTR, T>(sb[buf], wj * 64 + 32 * n, k);
-            }
+        for (int m = 0; m < NB; ++m) fb[to][m] = fragment<BTR, TJ>(sb, piece_b(m), s);
+    };
+    auto multiply = [&](int from) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+        for (int m = 0; m < NA; ++m)
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[n], fb[m], acc[n][m], 0, 0, 0);
+            for (int k = 0; k < NB; ++k)
+                acc[m][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[from][m], fb[from][k], acc[m][k], 0, 0, 0);
+    };
+    // every wavefront has its loads in LDS and has read the image that is freed
+    auto meet = [&]() {
+        __builtin_amdgcn_s_waitcnt(0x0070);          // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+    };
+    // step k from image (a, b); the other image receives step k + 1, then this one k + 2
+    auto do_step = [&](int64_t k, uint16_t *a, uint16_t *b, uint16_t *na, uint16_t *nb) {
+        read(1, a, b, 1);
+        multiply(0);
+        read(0, a, b, 2);
+        multiply(1);
+        read(1, a, b, 3);
+        multiply(0);
+        if (k + 1 < n) {
+            la.put(na);
+            lb.put(nb);
         }
-        if (s + 1 < s1) put(buf ^ 1);
+        meet();
+        if (k + 2 < n) start(k + 2, a, b);
+        if (k + 1 < n) read(0, na, nb, 0);
+        multiply(1);
+    };
+    if (n > 0) {
+        start(0, sa0, sb0);
+        la.put(sa0);
+        lb.put(sb0);
+        meet();
+        if (n > 1) start(1, sa1, sb1);
+        read(0, sa0, sb0, 0);
+        for (int64_t k = 0; k < n; k += 2) {
+            do_step(k, sa0, sb0, sa1, sb1);
+            if (k + 1 < n) do_step(k + 1, sa1, sb1, sa0, sb0);
+        }
     }
 
     // lane: output row j = lane % 32, output columns 8 q + 4 (lane / 32) + 0..3 for q < 4
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        const int64_t j = j0 + wj * 64 + 32 * m + (lane & 31);
+    for (int m = 0; m < NB; ++m) {
+        const int64_t j = j0 + piece_b(m) + (lane & 31);
+        const bool row_ok = j < g.J;
         if constexpr (KIND == kGemmGated) {
-            const int64_t i = i0 + wi * 32 + 4 * (lane >> 5);
-            float gv[16], uv[16], hv[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                gv[e] = acc[0][m][e];
-                uv[e] = acc[1][m][e];
-                float act, dact;
-                activation(g.act, gv[e], act, dact);
-                hv[e] = act * uv[e];
+            for (int p = 0; p < NA / 2; ++p) {
+                const int64_t i = i0 + piece_a(p);
+                float gv[16], uv[16], hv[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    gv[e] = acc[p][m][e];
+                    uv[e] = acc[p + NA / 2][m][e];
+                    float act, dact;
+                    activation(g.act, gv[e], act, dact);
+                    hv[e] = act * uv[e];
+                }
+                store_row(static_cast<uint16_t *>(g.out[0].p) + j * g.out[0].ld, i, g.I, row_ok, hv);
+                keep_row(g.gate, j, i, g.I, row_ok, gv);
+                keep_row(g.up, j, i, g.I, row_ok, uv);
             }
-            const bool row_ok = j < g.J;
-            auto dense = [&](const Mat &o, const float *v) {
-                if (!row_ok) return;
-                uint16_t *p = static_cast<uint16_t *>(o.p) + j * o.ld;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int64_t col = i + 8 * (e >> 2) + (e & 3);
-                    if (col < g.I) p[col] = static_cast<uint16_t>(to_bf16(v[e]));
-                }
-            };
-            // lanes l and l + 32 hold one scale group (32 columns of a row) between them
-            auto keep = [&](const Mat &o, float *v) {
-                if (o.p == nullptr) return;
-                if (o.dt == FSDPPACK_BF16) return dense(o, v);
-                float top = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, finite(v[e]) ? fabsf(v[e]) : 0.0f);
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const int ex = o.dt == FSDPPACK_E4M3 ? scale_exponent<FSDPPACK_E4M3>(top) : scale_exponent<FSDPPACK_INT8>(top);
-                uint32_t w[4];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (o.dt == FSDPPACK_E4M3) encode8<FSDPPACK_E4M3>(v + 8 * q, ex, w[2 * q], w[2 * q + 1]);
-                    else encode8<FSDPPACK_INT8>(v + 8 * q, ex, w[2 * q], w[2 * q + 1]);
-                }
-                if (!row_ok) return;
-                uint8_t *p = static_cast<uint8_t *>(o.p) + j * o.ld;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int64_t col = i + 8 * (e >> 2) + (e & 3);
-                    if (col < g.I) p[col] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
-                }
-                if (lane < 32 && i < g.I) o.scales[j * ((g.I + kGroup - 1) / kGroup) + i / kGroup] = static_cast<uint8_t>(ex + 127);
-            };
-            dense(g.out[0], hv);
-            keep(g.gate, gv);
-            keep(g.up, uv);
         } else {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int64_t i = i0 + ia[n] + 4 * (lane >> 5);
-                if (j >= g.J) continue;
+            for (int p = 0; p < NA; ++p) {
+                const int64_t i = i0 + piece_a(p);
+                float v[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int64_t col = i + 8 * (e >> 2) + (e & 3);
-                    if (col >= g.I) continue;
-                    if (g.splits > 1)
-                        g.partial[((int64_t{z} * g.splits + split) * g.J + j) * g.I + col] = acc[n][m][e];
-                    else if (g.out[z].dt == FSDPPACK_BF16)
-                        static_cast<uint16_t *>(g.out[z].p)[j * g.out[z].ld + col] = static_cast<uint16_t>(to_bf16(acc[n][m][e]));
-                    else
-                        static_cast<float *>(g.out[z].p)[j * g.out[z].ld + col] = acc[n][m][e];
-                }
+                for (int e = 0; e < 16; ++e) v[e] = acc[p][m][e];
+                const Mat &o = g.out[z];
+                if (g.splits > 1) store_row_fp32(g.partial + ((int64_t{z} * g.splits + split) * g.J + j) * g.I, i, g.I, row_ok, v);
+                else if (o.dt == FSDPPACK_BF16) store_row(static_cast<uint16_t *>(o.p) + j * o.ld, i, g.I, row_ok, v);
+                else store_row_fp32(static_cast<float *>(o.p) + j * o.ld, i, g.I, row_ok, v);
             }
         }
     }
+#endif
 }
 
 // The splits' partial sums, in a fixed order, rounded once.
@@ -268,19 +434,57 @@ int gemm_splits(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
     return 1;
 }
 
+namespace {
+
+// Rows that 16-byte chunks can be taken from whole: `width` elements of a row
+// are read in chunks.
+bool whole_chunks(const Mat &m, int64_t width)
+{
+    return m.dt == FSDPPACK_BF16 && reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0 && width % 8 == 0;
+}
+
+template <GemmKind KIND, int ADT, bool DMA_A, bool DMA_B>
+int launch_tiles(GemmArgs &g, void *stream, void *e0, void *e1)
+{
+    constexpr int TI = 256, TJ = 256, WI = 2, WJ = 4;
+    constexpr int step_i = KIND == kGemmGated ? TI / 2 : TI;
+    g.tiles_i = static_cast<int32_t>((g.I + step_i - 1) / step_i);
+    g.tiles_j = static_cast<int32_t>((g.J + TJ - 1) / TJ);
+    const int64_t tiles = int64_t{g.tiles_i} * g.tiles_j * g.splits * g.outs;
+    const dim3 grid(static_cast<uint32_t>((tiles + kXcds - 1) / kXcds * kXcds)), block(64 * WI * WJ);
+    LAUNCH((gemm_kernel<KIND, ADT, DMA_A, DMA_B, TI, TJ, WI, WJ>), grid, block, g);
+    return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace
+
 int launch_gemm(GemmKind kind, GemmArgs g, void *stream, void *e0, void *end, int *launches)
 {
-    const int ti = kind == kGemmGated ? T / 2 : T;
-    g.tiles_i = static_cast<int32_t>((g.I + ti - 1) / ti);
-    g.tiles_j = static_cast<int32_t>((g.J + T - 1) / T);
     void *e1 = g.splits > 1 ? nullptr : end;
-    const dim3 grid(static_cast<uint32_t>(int64_t{g.tiles_i} * g.tiles_j * g.splits * g.outs)), block(kBlockThreads);
-    if (kind == kGemmGated) LAUNCH((gemm_kernel<kGemmGated, FSDPPACK_BF16>), grid, block, g);
-    else if (kind == kGemmDx) LAUNCH((gemm_kernel<kGemmDx, FSDPPACK_BF16>), grid, block, g);
-    else if (g.a[0].dt == FSDPPACK_BF16) LAUNCH((gemm_kernel<kGemmDw, FSDPPACK_BF16>), grid, block, g);
-    else if (g.a[0].dt == FSDPPACK_E4M3) LAUNCH((gemm_kernel<kGemmDw, FSDPPACK_E4M3>), grid, block, g);
-    else LAUNCH((gemm_kernel<kGemmDw, FSDPPACK_INT8>), grid, block, g);
+    const int64_t wa = kind == kGemmGated ? g.R : g.I, wb = kind == kGemmDw ? g.J : g.R;
+    const bool two_a = kind != kGemmDw, two_b = kind == kGemmDx || g.outs == 2;
+    const bool dma_a = whole_chunks(g.a[0], wa) && (!two_a || (whole_chunks(g.a[1], wa) && g.a[1].ld == g.a[0].ld));
+    const bool dma_b = whole_chunks(g.b[0], wb) && (!two_b || whole_chunks(g.b[1], wb));
+    const bool dma = dma_a && dma_b;
+    const int adt = g.a[0].dt;
+    int rc;
+    if (kind == kGemmGated)
+        rc = dma ? launch_tiles<kGemmGated, FSDPPACK_BF16, true, true>(g, stream, e0, e1)
+                 : launch_tiles<kGemmGated, FSDPPACK_BF16, false, false>(g, stream, e0, e1);
+    else if (kind == kGemmDx)
+        rc = dma ? launch_tiles<kGemmDx, FSDPPACK_BF16, true, true>(g, stream, e0, e1)
+                 : launch_tiles<kGemmDx, FSDPPACK_BF16, false, false>(g, stream, e0, e1);
+    else if (adt == FSDPPACK_BF16)
+        rc = dma ? launch_tiles<kGemmDw, FSDPPACK_BF16, true, true>(g, stream, e0, e1)
+                 : launch_tiles<kGemmDw, FSDPPACK_BF16, false, false>(g, stream, e0, e1);
+    else if (adt == FSDPPACK_E4M3)
+        rc = dma_b ? launch_tiles<kGemmDw, FSDPPACK_E4M3, false, true>(g, stream, e0, e1)
+                   : launch_tiles<kGemmDw, FSDPPACK_E4M3, false, false>(g, stream, e0, e1);
+    else
+        rc = dma_b ? launch_tiles<kGemmDw, FSDPPACK_INT8, false, true>(g, stream, e0, e1)
+                   : launch_tiles<kGemmDw, FSDPPACK_INT8, false, false>(g, stream, e0, e1);
     *launches = 1;
+    if (rc != 0) return rc;
     if (g.splits > 1) {
         e0 = nullptr;
         e1 = end;
