@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fsdppack_train_device.h"
 
@@ -32,14 +33,45 @@ constexpr int BK = 64;               // reduction elements per step
 constexpr int kXcds = 8;             // workgroups go round-robin over 8 dies, each with its own L2
 
 // Where a chunk of 8 elements lies in a tile's LDS image (in elements).
-//  reduction contiguous: [T][64], 8 chunks a row, chunk c at c ^ (row & 7)
+//  reduction contiguous: [T][64], 8 chunks a row, chunk c at c ^ (row / 2 & 7)
 //  reduction strided:    [64][T], T / 8 chunks a row, chunk c at c ^ 4 (row & 3)
-// so that the 16-byte reads of 8 rows, and the 64-byte pieces of 4 rows that a
-// transposing read takes at once, fall into different banks.
+// so that the 16-byte reads of 16 rows, and the 64-byte pieces of 4 rows that
+// a transposing read takes at once, fall into different banks (of 64, 256
+// bytes in all: what LDS delivers in a cycle).
 template <bool TR, int T>
 __device__ __forceinline__ int swizzled(int row, int chunk)
 {
-    return TR ? chunk ^ ((row & 3) << 2) : chunk ^ (row & 7);
+    return TR ? chunk ^ ((row & 3) << 2) : chunk ^ (row >> 1 & 7);
+}
+
+// Eight codes as bf16, exactly.  E4M3: the hardware's scaled conversion.
+// INT8: code + 128 is an unsigned byte u, and u * scale - 128 * scale is exact
+// in one fused step; u = 0 stands for "not finite".
+template <int DT>
+__device__ __forceinline__ u32x4 decode8_bf16(uint32_t lo, uint32_t hi, float scale)
+{
+    u32x4 o;
+    if constexpr (DT == FSDPPACK_E4M3) {
+        o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false));
+        o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true));
+        o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
+        o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
+    } else {
+        const uint32_t a = lo ^ 0x80808080u, b = hi ^ 0x80808080u;
+        const float off = -128.0f * scale;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(static_cast<float>(((i < 4 ? a : b) >> (8 * (i & 3))) & 0xffu), scale, off);
+        // a zero byte is the code -128
+        if ((((a - 0x01010101u) & ~a) | ((b - 0x01010101u) & ~b)) & 0x80808080u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((((i < 4 ? a : b) >> (8 * (i & 3))) & 0xffu) == 0) v[i] = __builtin_nanf("");
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1]), __float_as_uint(v[2 * i]), 0x07060302u);
+    }
+    return o;
 }
 
 // One operand's tile of T x 64 elements, brought into LDS by THREADS threads.
@@ -65,69 +97,103 @@ struct Loader {
     u32x4 reg[DMA ? 1 : kUnits];
     uint32_t scale[DT == FSDPPACK_BF16 ? 1 : kUnits];
 
-    // Start reading the tile whose first reduction element is r0 and whose
-    // first row (column, TR) is t0; R and W bound the two.
-    __device__ __forceinline__ void start(const Mat &m, const Mat &m2, int64_t t0, int64_t r0, int64_t W, int64_t R, uint16_t *lds)
+    // Where the next step's tile starts, and each unit's offset from there in bytes.
+    const char *at, *at2;
+    const uint8_t *scale_at;
+    int64_t pitch, scale_pitch;
+    uint32_t off[kUnits], scale_off[DT == FSDPPACK_BF16 ? 1 : kUnits];
+
+    // Set out at reduction element r0 of the tile whose first row (column,
+    // TR) is t0, of W.
+    __device__ __forceinline__ void seek(const Mat &m, const Mat &m2, int64_t t0, int64_t r0, int64_t W)
     {
-        const int tid = threadIdx.x;
-        const int row0 = tid * kUnit / kPerRow, col0 = tid * kUnit % kPerRow;
-        if constexpr (DMA) {
-            const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-            const int64_t first = TR ? r0 * m.ld + t0 : t0 * m.ld + r0;
-            auto rsrc = [&](const Mat &x) {
-                return __builtin_amdgcn_make_buffer_rsrc(static_cast<uint16_t *>(x.p) + first, 0, 0x7fffffff, 0x00020000);
-            };
-            const auto b0 = rsrc(m);
-            const auto b1 = rsrc(m2);
-            const int32_t ld = static_cast<int32_t>(m.ld);
-            const int32_t nt = static_cast<int32_t>(W - t0 < T ? W - t0 : T), nr = static_cast<int32_t>(R - r0 < BK ? R - r0 : BK);
+        constexpr int SIZE = DT == FSDPPACK_BF16 ? 2 : 1;
+        const int row0 = threadIdx.x * kUnit / kPerRow, col0 = threadIdx.x * kUnit % kPerRow;
+        const int64_t first = (TR ? r0 * m.ld + t0 : t0 * m.ld + r0) * SIZE;
+        at = static_cast<const char *>(m.p) + first;
+        if constexpr (TWO) at2 = static_cast<const char *>(m2.p) + (t0 * m2.ld + r0) * SIZE;
+        pitch = (TR ? BK * m.ld : BK) * SIZE;
+        const int32_t nt = static_cast<int32_t>(W - t0 < T ? W - t0 : T);
 #pragma unroll
-            for (int c = 0; c < kUnits; ++c) {
-                const int row = row0 + c * kRows;
-                const int col = swizzled<TR, T>(row, col0 >> 3) << 3;
-                const int r = TWO ? row & (T / 2 - 1) : row;
-                const bool in = TR ? r < nr && col < nt : r < nt && col < nr;
-                const uint32_t off = in ? static_cast<uint32_t>(r * ld + col) * 2u : kOutside;
-                auto *to = (__attribute__((address_space(3))) void *)(lds + (wave * 64 + c * THREADS) * 8);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(TWO && c * kRows >= T / 2 ? b1 : b0, to, 16, off, 0, 0, 0);
+        for (int c = 0; c < kUnits; ++c) {
+            const int32_t ld = static_cast<int32_t>(TWO && c * kRows >= T / 2 ? m2.ld : m.ld);
+            const int row = row0 + c * kRows, col = DMA ? swizzled<TR, T>(row, col0 >> 3) << 3 : col0;
+            const int r = TWO ? row & (T / 2 - 1) : row;
+            off[c] = !DMA || (TR ? col : r) < nt ? static_cast<uint32_t>(r * ld + col) * SIZE : kOutside;
+        }
+        if constexpr (DT != FSDPPACK_BF16) {
+            static_assert(TR, "8-bit operands have their scale groups across the tile");
+            const int32_t groups = static_cast<int32_t>((W + kGroup - 1) / kGroup);
+            scale_at = m.scales + r0 * groups + t0 / kGroup;
+            scale_pitch = int64_t{BK} * groups;
+#pragma unroll
+            for (int c = 0; c < kUnits; ++c) scale_off[c] = (row0 + c * kRows) * groups + col0 / kGroup;
+        }
+    }
+
+    // Start bringing in the step at which the loader stands, and go on to the
+    // next.  `left`: reduction elements from there on; WHOLE: BK at least.
+    template <bool WHOLE>
+    __device__ __forceinline__ void start_dma(int64_t left, uint16_t *lds)
+    {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        auto rsrc = [](const char *p) {
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, 0x7fffffff, 0x00020000);
+        };
+        const auto b0 = rsrc(at);
+        const auto b1 = rsrc(TWO ? at2 : at);
+#pragma unroll
+        for (int c = 0; c < kUnits; ++c) {
+            uint32_t o = off[c];
+            if constexpr (!WHOLE) {
+                const int row = threadIdx.x * kUnit / kPerRow + c * kRows;
+                const int col = swizzled<TR, T>(row, threadIdx.x * kUnit % kPerRow >> 3) << 3;
+                if ((TR ? row : col) >= left) o = kOutside;
             }
-        } else {
+            auto *to = (__attribute__((address_space(3))) void *)(lds + (wave * 64 + c * THREADS) * 8);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(TWO && c * kRows >= T / 2 ? b1 : b0, to, 16, o, 0, 0, 0);
+        }
+        at += pitch;
+        if constexpr (TWO) at2 += pitch;
+    }
+
+    // The same through registers.  `rest`: rows (columns, TR) of the tile
+    // that exist; WHOLE: all of them, and BK reduction elements.
+    template <bool WHOLE>
+    __device__ __forceinline__ void start_reg(int64_t left, int64_t rest)
+    {
+        typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
+        typedef std::conditional_t<DT == FSDPPACK_BF16, u32x4u, u32x4b> Wide;
+        constexpr int SIZE = DT == FSDPPACK_BF16 ? 2 : 1;
 #pragma unroll
-            for (int c = 0; c < kUnits; ++c) {
-                const int row = row0 + c * kRows;
-                const Mat &x = TWO && c * kRows >= T / 2 ? m2 : m;
-                const int r = TWO ? row & (T / 2 - 1) : row;
-                const int64_t mr = TR ? r0 + r : t0 + r, mc = (TR ? t0 : r0) + col0;
-                const int64_t rows = TR ? R : W, cols = TR ? W : R;
-                reg[c] = u32x4{0, 0, 0, 0};
-                if constexpr (DT != FSDPPACK_BF16) scale[c] = 0;
-                if (mr < rows && mc < cols) {
-                    if constexpr (DT == FSDPPACK_BF16) {
-                        const uint16_t *p = static_cast<const uint16_t *>(x.p) + mr * x.ld + mc;
-                        if (mc + 8 <= cols) {
-                            const u32x4u w = *reinterpret_cast<const u32x4u *>(p);
-                            reg[c] = u32x4{w.x, w.y, w.z, w.w};
-                        } else {
+        for (int c = 0; c < kUnits; ++c) {
+            const char *p = (TWO && c * kRows >= T / 2 ? at2 : at) + off[c];
+            int n = kUnit;                            // elements of the unit that exist
+            if constexpr (!WHOLE) {
+                const int row = threadIdx.x * kUnit / kPerRow + c * kRows, col0 = threadIdx.x * kUnit % kPerRow;
+                const int64_t rows = TR ? left : rest, cols = (TR ? rest : left) - col0;
+                n = (TWO ? row & (T / 2 - 1) : row) >= rows || cols <= 0 ? 0 : cols < kUnit ? static_cast<int>(cols) : kUnit;
+            }
+            reg[c] = u32x4{0, 0, 0, 0};
+            if constexpr (DT != FSDPPACK_BF16) scale[c] = 0;
+            if (WHOLE || n == kUnit) {
+                const Wide w = *reinterpret_cast<const Wide *>(p);
+                reg[c] = u32x4{w.x, w.y, w.z, w.w};
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t v = SIZE == 2 ? *reinterpret_cast<const uint16_t *>(p + 2 * i) : *reinterpret_cast<const uint8_t *>(p + i);
+                    const uint32_t bits = v << (8 * SIZE * (i % (4 / SIZE)));
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (mc + i < cols) reg[c][i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
-                        }
-                    } else {
-                        const uint8_t *p = static_cast<const uint8_t *>(x.p) + mr * x.ld + mc;
-                        if (mc + 16 <= cols) {
-                            typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
-                            const u32x4b w = *reinterpret_cast<const u32x4b *>(p);
-                            reg[c] = u32x4{w.x, w.y, w.z, w.w};
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (mc + i < cols) reg[c][i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-                        }
-                        scale[c] = x.scales[mr * ((cols + kGroup - 1) / kGroup) + mc / kGroup];
-                    }
+                    for (int d = 0; d < 4; ++d) reg[c][d] |= i / (4 / SIZE) == d ? bits : 0u;
                 }
             }
+            if constexpr (DT != FSDPPACK_BF16)
+                if (WHOLE || n > 0) scale[c] = scale_at[scale_off[c]];
         }
+        at += pitch;
+        if constexpr (TWO) at2 += pitch;
+        if constexpr (DT != FSDPPACK_BF16) scale_at += scale_pitch;
     }
 
     // Write the registers' tile to LDS.
@@ -143,10 +209,7 @@ struct Loader {
                 for (int h = 0; h < kUnit / 8; ++h) {
                     u32x4 o = reg[c];
                     if constexpr (DT != FSDPPACK_BF16) {
-                        float v[8];
-                        decode8<DT>(reg[c][2 * h], reg[c][2 * h + 1], scale_of(static_cast<uint8_t>(scale[c])), v);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                        o = decode8_bf16<DT>(reg[c][2 * h], reg[c][2 * h + 1], __uint_as_float(scale[c] << 23));
                     }
                     *reinterpret_cast<u32x4 *>(lds + row * kPerRow + (swizzled<TR, T>(row, (col0 >> 3) + h) << 3)) = o;
                 }
@@ -274,7 +337,7 @@ __device__ __forceinline__ void keep_row(const Mat &o, int64_t j, int64_t col, i
 // that neither the barrier nor LDS nor memory latency leaves the matrix cores
 // idle.
 template <GemmKind KIND, int ADT, bool DMA_A, bool DMA_B, int TI, int TJ, int WI, int WJ>
-__global__ void __launch_bounds__(64 * WI * WJ, TI == 256 ? 2 : 2) gemm_kernel(GemmArgs g)
+__global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(GemmArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)      // the body uses device builtins that the host's pass does not know
     constexpr bool ATR = KIND != kGemmGated, BTR = KIND == kGemmDw;
@@ -303,13 +366,25 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 ? 2 : 2) gemm_kernel(G
 
     Loader<ATR, TI, THREADS, ADT, DMA_A, KIND == kGemmGated> la;
     Loader<BTR, TJ, THREADS, FSDPPACK_BF16, DMA_B, false> lb;
-    auto start = [&](int64_t k, uint16_t *sa, uint16_t *sb) {
+    const int64_t whole1 = g.R / BK;                    // whole steps of a segment
+    const auto &first_b = g.b[KIND == kGemmDw ? z : 0];
+    // a tile read through registers has all of its rows and columns
+    const bool inside = (DMA_A || i_end - i0 >= (KIND == kGemmGated ? TI / 2 : TI)) && (DMA_B || g.J - j0 >= TJ);
+    // bring in step k; WHOLE: it is a whole step and not a segment's first
+    auto start = [&](auto whole, int64_t k, uint16_t *sa, uint16_t *sb) {
+        constexpr bool WHOLE = decltype(whole)::value;
         const int64_t step = s0 + k;
-        const int seg = step >= steps1;
+        const int seg = KIND == kGemmDx && step >= steps1;
         const int64_t r0 = (step - seg * steps1) * BK;
-        la.start(g.a[seg], KIND == kGemmGated ? g.a[1] : g.a[seg], i0, r0, i_end, g.R, sa);
-        const Mat &b = g.b[KIND == kGemmDw ? z : seg];
-        lb.start(b, b, j0, r0, g.J, g.R, sb);
+        const Mat &b = KIND == kGemmDw ? first_b : g.b[seg];
+        if (!WHOLE && (k == 0 || r0 == 0)) {
+            la.seek(g.a[seg], KIND == kGemmGated ? g.a[1] : g.a[seg], i0, r0, i_end);
+            lb.seek(b, b, j0, r0, g.J);
+        }
+        if constexpr (DMA_A) la.template start_dma<WHOLE>(g.R - r0, sa);
+        else la.template start_reg<WHOLE>(g.R - r0, i_end - i0);
+        if constexpr (DMA_B) lb.template start_dma<WHOLE>(g.R - r0, sb);
+        else lb.template start_reg<WHOLE>(g.R - r0, g.J - j0);
     };
 
     const int wi = wave % WI, wj = wave / WI;
@@ -334,38 +409,65 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 ? 2 : 2) gemm_kernel(G
             for (int k = 0; k < NB; ++k)
                 acc[m][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[from][m], fb[from][k], acc[m][k], 0, 0, 0);
     };
+    // a slice's LDS reads go between its matrix instructions, not before them
+    auto mix = [&]() {
+        constexpr int reads = NA * (ATR ? 2 : 1) + NB * (BTR ? 2 : 1), mm = NA * NB;
+        constexpr int per = (reads + mm - 1) / mm;
+#pragma unroll
+        for (int i = 0; i < mm; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // one matrix instruction,
+            __builtin_amdgcn_sched_group_barrier(0x100, per, 0);    // its share of the LDS reads
+        }
+    };
     // every wavefront has its loads in LDS and has read the image that is freed
     auto meet = [&]() {
         __builtin_amdgcn_s_waitcnt(0x0070);          // vmcnt(0) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
     };
-    // step k from image (a, b); the other image receives step k + 1, then this one k + 2
-    auto do_step = [&](int64_t k, uint16_t *a, uint16_t *b, uint16_t *na, uint16_t *nb) {
+    // step k from image (a, b); the other image receives step k + 1, then this
+    // one k + 2.  WHOLE: both exist, and k + 2 is whole and not a segment's first
+    auto do_step = [&](auto whole, int64_t k, uint16_t *a, uint16_t *b, uint16_t *na, uint16_t *nb) {
+        constexpr bool WHOLE = decltype(whole)::value;
         read(1, a, b, 1);
         multiply(0);
+        mix();
         read(0, a, b, 2);
         multiply(1);
+        mix();
         read(1, a, b, 3);
         multiply(0);
-        if (k + 1 < n) {
+        mix();
+        if (WHOLE || k + 1 < n) {
             la.put(na);
             lb.put(nb);
         }
         meet();
-        if (k + 2 < n) start(k + 2, a, b);
-        if (k + 1 < n) read(0, na, nb, 0);
+        if (WHOLE || k + 2 < n) start(whole, k + 2, a, b);
+        if (WHOLE || k + 1 < n) read(0, na, nb, 0);
         multiply(1);
+        mix();
     };
+    constexpr std::true_type plain{};
+    constexpr std::false_type any{};
     if (n > 0) {
-        start(0, sa0, sb0);
+        start(any, 0, sa0, sb0);
         la.put(sa0);
         lb.put(sb0);
         meet();
-        if (n > 1) start(1, sa1, sb1);
+        if (n > 1) start(any, 1, sa1, sb1);
         read(0, sa0, sb0, 0);
-        for (int64_t k = 0; k < n; k += 2) {
-            do_step(k, sa0, sb0, sa1, sb1);
-            if (k + 1 < n) do_step(k + 1, sa1, sb1, sa0, sb0);
+        for (int64_t k = 0; k < n;) {
+            // pairs of steps from here that bring in whole steps of the same segment
+            const int64_t next = s0 + k + 2;
+            const int seg = KIND == kGemmDx && next >= steps1;
+            const int64_t end = seg * steps1 + whole1;
+            int64_t pairs = inside && next > seg * steps1 ? ((end - s0 < n ? end - s0 : n) - (k + 2)) / 2 : 0;
+            for (; pairs > 0; --pairs, k += 2) {
+                do_step(plain, k, sa0, sb0, sa1, sb1);
+                do_step(plain, k + 1, sa1, sb1, sa0, sb0);
+            }
+            do_step(any, k, sa0, sb0, sa1, sb1);
+            if (++k < n) do_step(any, k, sa1, sb1, sa0, sb0), ++k;
         }
     }
 
@@ -463,7 +565,7 @@ int launch_gemm(GemmKind kind, GemmArgs g, void *stream, void *e0, void *end, in
     void *e1 = g.splits > 1 ? nullptr : end;
     const int64_t wa = kind == kGemmGated ? g.R : g.I, wb = kind == kGemmDw ? g.J : g.R;
     const bool two_a = kind != kGemmDw, two_b = kind == kGemmDx || g.outs == 2;
-    const bool dma_a = whole_chunks(g.a[0], wa) && (!two_a || (whole_chunks(g.a[1], wa) && g.a[1].ld == g.a[0].ld));
+    const bool dma_a = whole_chunks(g.a[0], wa) && (!two_a || whole_chunks(g.a[1], wa));
     const bool dma_b = whole_chunks(g.b[0], wb) && (!two_b || whole_chunks(g.b[1], wb));
     const bool dma = dma_a && dma_b;
     const int adt = g.a[0].dt;
