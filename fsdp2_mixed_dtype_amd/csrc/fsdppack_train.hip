@@ -11,44 +11,95 @@
 namespace fsdppack {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kThreads = 256;
 
-// Sum over the block's four wavefronts.
-__device__ __forceinline__ float block_sum(float v, float *s)
-{
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (s[0] + s[1]) + (s[2] + s[3]);
-}
+// Where a thread's units of `SIZE` columns lie.  FLAT: rows follow one another
+// without gaps and no row ends inside a unit (or inside a scale group, where
+// there is one), so that the matrix is one long row; otherwise a unit's row
+// comes from a division by a launch constant (multiply and shift).
+struct Rows {
+    int64_t units;                    // units in all
+    uint32_t per_row, magic, shift;   // n / per_row = n * magic >> shift for n < 2^31
+};
 
-// One group of eight columns per thread and step; a row of ceil(cols / 32)
-// groups of four such threads, so that a checkpoint's scale group never
-// crosses a row's end.
-template <int XT>
-__global__ void __launch_bounds__(kThreads) save_kernel(Mat x, Mat q, int64_t rows, int32_t cols)
+template <bool FLAT>
+__device__ __forceinline__ void unit_at(const Rows &w, int64_t base, int32_t local, int64_t base_row, uint32_t base_unit, int64_t &row,
+                                        int32_t &unit)
 {
-    const int32_t units = (cols + kGroup - 1) / kGroup * 4;
-    for (int64_t t = int64_t{blockIdx.x} * kThreads + threadIdx.x; t < rows * units; t += int64_t{gridDim.x} * kThreads) {
-        const int64_t r = t / units;
-        const int32_t col = static_cast<int32_t>(t - r * units) * 8;
-        float v[8];
-        load8<XT>(row_of(x, r), nullptr, col, cols, v);
-        save8(q, r, col, cols, v);
+    if constexpr (FLAT) {
+        row = 0;
+        unit = 0;
+    } else {
+        const uint32_t n = base_unit + static_cast<uint32_t>(local);
+        const uint32_t q = static_cast<uint32_t>((uint64_t{n} * w.magic) >> w.shift);
+        row = base_row + q;
+        unit = static_cast<int32_t>(n - q * w.per_row);
     }
 }
 
-template <int QT>
-__global__ void __launch_bounds__(kThreads) load_kernel(Mat q, Mat out, int64_t rows, int32_t cols)
+// A block takes kSpan units in a row, kEach of every thread's; its first unit's
+// row is found once.
+constexpr int kEach = 4, kSpan = kThreads * kEach;
+
+template <int XT, int QT, bool FLAT>
+__global__ void __launch_bounds__(kThreads) save_kernel(Mat x, Mat q, Rows w, int32_t cols)
 {
-    const int32_t units = (cols + 7) / 8;
-    for (int64_t t = int64_t{blockIdx.x} * kThreads + threadIdx.x; t < rows * units; t += int64_t{gridDim.x} * kThreads) {
-        const int64_t r = t / units;
-        const int32_t col = static_cast<int32_t>(t - r * units) * 8;
-        float v[8];
-        load8<QT>(row_of(q, r), q.scales + r * ((cols + kGroup - 1) / kGroup), col, cols, v);
-        store8(row_of_out(out, r), out.dt, col, cols, v);
+    const int64_t base = int64_t{blockIdx.x} * kSpan;
+    const int64_t base_row = FLAT ? 0 : base / w.per_row;
+    const uint32_t base_unit = FLAT ? 0 : static_cast<uint32_t>(base - base_row * w.per_row);
+    float v[kEach][8];
+    int64_t row[kEach];
+    int32_t unit[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int32_t local = e * kThreads + threadIdx.x;
+        const int64_t t = base + local;
+        if (t >= w.units) continue;
+        unit_at<FLAT>(w, base, local, base_row, base_unit, row[e], unit[e]);
+        if constexpr (FLAT) load8<XT>(static_cast<const char *>(x.p) + t * (XT == FSDPPACK_BF16 ? 16 : 32), nullptr, 0, 8, v[e]);
+        else load8<XT>(row_of(x, row[e]), nullptr, unit[e] * 8, cols, v[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int64_t t = base + e * kThreads + threadIdx.x;
+        if (t >= w.units) continue;       // the same for the four threads of a group
+        uint8_t *p = static_cast<uint8_t *>(q.p);
+        if constexpr (FLAT) {
+            save8_as<QT>(p + (t >> 2) * kGroup, q.scales + (t >> 2), static_cast<int32_t>(t & 3) * 8, kGroup, v[e]);
+        } else {
+            const int32_t groups = (cols + kGroup - 1) / kGroup;
+            save8_as<QT>(p + row[e] * q.ld, q.scales + row[e] * groups, unit[e] * 8, cols, v[e]);
+        }
+    }
+}
+
+template <int QT, bool FLAT>
+__global__ void __launch_bounds__(kThreads) load_kernel(Mat q, Mat out, Rows w, int32_t cols)
+{
+    const int64_t base = int64_t{blockIdx.x} * kSpan;
+    const int64_t base_row = FLAT ? 0 : base / w.per_row;
+    const uint32_t base_unit = FLAT ? 0 : static_cast<uint32_t>(base - base_row * w.per_row);
+    float v[kEach][8];
+    int64_t row[kEach];
+    int32_t unit[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int32_t local = e * kThreads + threadIdx.x;
+        const int64_t t = base + local;
+        if (t >= w.units) continue;
+        unit_at<FLAT>(w, base, local, base_row, base_unit, row[e], unit[e]);
+        if constexpr (FLAT) load8<QT>(static_cast<const char *>(q.p) + t * 8, q.scales + (t >> 2), 0, 8, v[e]);
+        else load8<QT>(row_of(q, row[e]), q.scales + row[e] * ((cols + kGroup - 1) / kGroup), unit[e] * 8, cols, v[e]);
+    }
+    const int32_t size = out.dt == FSDPPACK_BF16 ? 16 : 32;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int64_t t = base + e * kThreads + threadIdx.x;
+        if (t >= w.units) continue;
+        if constexpr (FLAT) store8(static_cast<char *>(out.p) + t * size, out.dt, 0, 8, v[e]);
+        else store8(row_of_out(out, row[e]), out.dt, unit[e] * 8, cols, v[e]);
     }
 }
 
@@ -62,8 +113,120 @@ __device__ __forceinline__ void load_weight(const void *w, int32_t dt, int32_t c
     }
 }
 
-// One block per row; the row is read once for the mean, once for the spread
-// and once for the result (all but the first from cache).
+// Sums over the WAVES wavefronts that share a row, the same in each of their
+// lanes.  `s`: WAVES floats per sum and group of wavefronts; the caller
+// alternates between two such places, so that one barrier a row is enough.
+template <int WAVES, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float *s)
+{
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+    if constexpr (WAVES > 1) {
+        const int wave = (threadIdx.x >> 6) % WAVES;
+        float *mine = s + (threadIdx.x >> 6) / WAVES * (N * WAVES);
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) mine[k * WAVES + wave] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float sum = mine[k * WAVES];
+#pragma unroll
+            for (int i = 1; i < WAVES; ++i) sum += mine[k * WAVES + i];
+            v[k] = sum;
+        }
+    }
+}
+
+// A row in the registers of WAVES wavefronts, NV units of 8 columns a lane:
+// read once from memory, next row's loads under way while this one is summed.
+// Bound by memory.  A block of THREADS works on THREADS / 64 / WAVES rows at a
+// time and keeps the weights of its columns for all of its rows.
+template <int XT, int WAVES, int NV>
+__global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) norm_forward_rows_kernel(NormArgs a)
+{
+    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : kThreads, GROUPS = THREADS / 64 / WAVES;
+    __shared__ float s[2][2][GROUPS * WAVES];
+    const int32_t cols = a.cols;
+    const int lane = threadIdx.x % (64 * WAVES);
+    float w[NV][8], b[NV][8], v[NV][8], next[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int32_t c = (lane + k * 64 * WAVES) * 8;
+        load_weight(a.weight, a.wdt, c, cols, 1.0f, w[k]);
+        load_weight(a.bias, a.wdt, c, cols, 0.0f, b[k]);
+    }
+    const int64_t step = int64_t{gridDim.x} * GROUPS;
+    int64_t r = int64_t{blockIdx.x} * GROUPS + threadIdx.x / (64 * WAVES);
+    auto read = [&](int64_t row) {
+        const void *x = row_of(a.x, row < a.rows ? row : a.rows - 1);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) load8<XT>(x, nullptr, (lane + k * 64 * WAVES) * 8, cols, next[k]);
+    };
+    const float inv = 1.0f / static_cast<float>(cols);
+    read(r);
+    // the same number of turns for all of a block's wavefronts (they meet in row_sums)
+    for (int64_t first = int64_t{blockIdx.x} * GROUPS, turn = 0; first < a.rows; first += step, r += step, ++turn) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[k][i] = next[k][i];
+        if (first + step < a.rows) read(r + step);
+        float mean = 0.0f;
+        if (!a.rms) {
+            float sum[1] = {0.0f};
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[0] += v[k][i];
+            row_sums<WAVES>(sum, s[0][turn & 1]);
+            mean = sum[0] * inv;
+        }
+        float sq[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t c = (lane + k * 64 * WAVES) * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = c + i < cols ? v[k][i] - mean : 0.0f;
+                sq[0] += d * d;
+            }
+        }
+        row_sums<WAVES>(sq, s[1][turn & 1]);
+        const float rstd = 1.0f / sqrtf(sq[0] * inv + a.eps);
+        if (r >= a.rows) continue;
+        if (lane == 0) {
+            a.stats[2 * r] = mean;
+            a.stats[2 * r + 1] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t c = (lane + k * 64 * WAVES) * 8;
+            if (c >= (cols + kGroup - 1) / kGroup * kGroup) continue;     // by whole groups of four lanes
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = c + i < cols ? (v[k][i] - mean) * rstd * w[k][i] + b[k][i] : 0.0f;
+            store8(row_of_out(a.out, r), a.out.dt, c, cols, y);
+            if (a.x_ckpt.p) save8(a.x_ckpt, r, c, cols, v[k]);
+            if (a.out_ckpt.p) save8(a.out_ckpt, r, c, cols, y);
+        }
+    }
+}
+
+// Sum over the block's four wavefronts.
+__device__ __forceinline__ float block_sum(float v, float *s)
+{
+    v = wave_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Rows too long for registers: one block per row; the row is read once for the
+// mean, once for the spread and once for the result (all but the first from
+// cache).
 template <int XT>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(NormArgs a)
 {
@@ -112,7 +275,156 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(NormArgs a)
 }
 
 // dx of a row: rstd * (w dy - c1 - xh c2), c1 and c2 the means of w dy and
-// w dy xh over the row (c1 = 0 for the RMS norm).
+// w dy xh over the row (c1 = 0 for the RMS norm).  As in the forward pass a row
+// lies in the registers of WAVES wavefronts; each lane also sums dy xh and dy
+// of its columns over the block's rows, and the block writes one partial sum a
+// column.  THREADS are many (512), so that few partial sums are written.
+template <int XT, int WAVES, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_backward_rows_kernel(NormBackArgs a)
+{
+    constexpr bool AHEAD = THREADS <= 512;       // 1024 threads have no registers for the next row's bits
+    constexpr int GROUPS = THREADS / 64 / WAVES;
+    constexpr bool EIGHT = XT == FSDPPACK_E4M3 || XT == FSDPPACK_INT8;
+    __shared__ float s[2][2 * GROUPS * WAVES];
+    __shared__ float joined[GROUPS > 1 ? 64 * WAVES * 8 : 1];
+    const int32_t cols = a.cols, groups = (cols + kGroup - 1) / kGroup;
+    const int lane = threadIdx.x % (64 * WAVES), group = threadIdx.x / (64 * WAVES);
+    float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
+    u32x4 nx[NV][XT == FSDPPACK_FP32 ? 2 : 1], nd[NV][2];
+    uint32_t nsc[NV] = {};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) load_weight(a.weight, a.wdt, (lane + k * 64 * WAVES) * 8, cols, 1.0f, w[k]);
+    const float inv = 1.0f / static_cast<float>(cols);
+    const bool wide_d = a.dout.dt == FSDPPACK_FP32;
+    // the bits of 8 elements from column c on; zeros past the row's end
+    auto bits = [&](const char *row, int size, int32_t c, u32x4 *o) {
+        const int32_t n = cols - c;
+        const char *p = row + int64_t{c} * size;
+        typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(2)));
+        if (size == 1) {
+            u32x2u q = {0, 0};
+            if (n >= 8) q = *reinterpret_cast<const u32x2u *>(p);
+            else
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n) q[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i & 3));
+            o[0] = u32x4{q.x, q.y, 0, 0};
+        } else if (size == 2) {
+            o[0] = u32x4{0, 0, 0, 0};
+            if (n >= 8) {
+                const u32x4b q = *reinterpret_cast<const u32x4b *>(p);
+                o[0] = u32x4{q.x, q.y, q.z, q.w};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n) o[0][i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << (16 * (i & 1));
+            }
+        } else {
+            o[0] = o[1] = u32x4{0, 0, 0, 0};
+            if (n >= 8) {
+                const u32x4b q = *reinterpret_cast<const u32x4b *>(p), t = *reinterpret_cast<const u32x4b *>(p + 16);
+                o[0] = u32x4{q.x, q.y, q.z, q.w};
+                o[1] = u32x4{t.x, t.y, t.z, t.w};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n) o[i >> 2][i & 3] = reinterpret_cast<const uint32_t *>(p)[i];
+            }
+        }
+    };
+    auto values = [](const u32x4 *o, bool wide, float *v) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = wide ? __uint_as_float(o[i >> 2][i & 3]) : (i & 1) ? bf16_hi(o[0][i >> 1]) : bf16_lo(o[0][i >> 1]);
+    };
+    float2 nst = {0.0f, 0.0f};
+    auto read = [&](int64_t row) {
+        row = row < a.rows ? row : a.rows - 1;
+        const char *x = static_cast<const char *>(row_of(a.x, row)), *d = static_cast<const char *>(row_of(a.dout, row));
+        nst = float2{a.stats[2 * row], a.stats[2 * row + 1]};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t c = (lane + k * 64 * WAVES) * 8;
+            bits(x, XT == FSDPPACK_FP32 ? 4 : XT == FSDPPACK_BF16 ? 2 : 1, c, nx[k]);
+            if constexpr (EIGHT) nsc[k] = c < cols ? a.x.scales[row * groups + c / kGroup] : 0;
+            if (wide_d) bits(d, 4, c, nd[k]);
+            else bits(d, 2, c, nd[k]);
+        }
+    };
+    const int64_t step = int64_t{gridDim.x} * GROUPS;
+    int64_t r = int64_t{blockIdx.x} * GROUPS + group;
+    if (AHEAD) read(r);
+    for (int64_t first = int64_t{blockIdx.x} * GROUPS, turn = 0; first < a.rows; first += step, r += step, ++turn) {
+        if (!AHEAD) read(r);
+        // xh and dy of the row; nothing of a row that is not there
+        float xh[NV][8], d[NV][8];
+        const float mean = nst.x, rstd = nst.y;
+        const bool there = r < a.rows;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t c = (lane + k * 64 * WAVES) * 8;
+            if constexpr (EIGHT) decode8<XT>(nx[k][0].x, nx[k][0].y, __uint_as_float(nsc[k] << 23), xh[k]);
+            else values(nx[k], XT == FSDPPACK_FP32, xh[k]);
+            values(nd[k], wide_d, d[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = there && c + i < cols;
+                xh[k][i] = in ? (xh[k][i] - mean) * rstd : 0.0f;
+                d[k][i] = in ? d[k][i] : 0.0f;
+                const float t = d[k][i] * w[k][i];
+                sum[0] += t * xh[k][i];
+                sum[1] += t;
+            }
+        }
+        if (AHEAD && first + step < a.rows) read(r + step);
+        row_sums<WAVES>(sum, s[turn & 1]);
+        const float c2 = sum[0] * inv, c1 = a.rms ? 0.0f : sum[1] * inv;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t c = (lane + k * 64 * WAVES) * 8;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[i] = rstd * (d[k][i] * w[k][i] - c1 - xh[k][i] * c2);
+                dw[k][i] += d[k][i] * xh[k][i];
+                db[k][i] += d[k][i];
+            }
+            if (there) store8(row_of_out(a.dx, r), a.dx.dt, c, cols, o);
+        }
+    }
+    if (a.partial == nullptr) return;
+    // the groups' sums, one after the other
+    float *p = a.partial + int64_t{blockIdx.x} * 2 * cols;
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t c = (lane + k * 64 * WAVES) * 8;
+            float *v = which ? db[k] : dw[k];
+            if constexpr (GROUPS > 1) {
+#pragma unroll 1
+                for (int from = 0; from < GROUPS; ++from) {
+                    if (group == from) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float *at = &joined[i * 64 * WAVES + lane];
+                            *at = from == 0 ? v[i] : *at + v[i];
+                        }
+                    }
+                    __syncthreads();
+                }
+                if (group == 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = joined[i * 64 * WAVES + lane];
+                }
+                __syncthreads();
+            }
+            if (group == 0) store8(p + which * cols, FSDPPACK_FP32, c, cols, v);
+        }
+}
+
+// Rows too long for registers: dx alone, the row read twice.
 template <int XT>
 __global__ void __launch_bounds__(kThreads) norm_dx_kernel(NormBackArgs a)
 {
@@ -151,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) norm_dx_kernel(NormBackArgs a)
     }
 }
 
-// Partial sums over a part of the rows of dy * xh and dy; thread = 8 columns.
+// Their partial sums over a part of the rows of dy * xh and dy; thread = 8 columns.
 template <int XT>
 __global__ void __launch_bounds__(64) norm_dw_kernel(NormBackArgs a)
 {
@@ -175,52 +487,81 @@ __global__ void __launch_bounds__(64) norm_dw_kernel(NormBackArgs a)
     store8(p + cols, FSDPPACK_FP32, c, cols, db);
 }
 
-// The parts' sums, in a fixed order: results do not depend on timing.
-__global__ void __launch_bounds__(kThreads) norm_join_kernel(NormBackArgs a)
+// The parts' sums, in a fixed order: results do not depend on timing.  64
+// columns a block, the parts dealt out over its 16 wavefronts.
+__global__ void __launch_bounds__(1024) norm_join_kernel(NormBackArgs a)
 {
-    const int64_t i = int64_t{blockIdx.x} * kThreads + threadIdx.x;
-    if (i >= int64_t{2} * a.cols) return;
-    void *dst = i < a.cols ? a.dweight : a.dbias;
+    __shared__ float s[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int32_t c = static_cast<int32_t>(blockIdx.x) * 64 + lane;
+    void *dst = blockIdx.y == 0 ? a.dweight : a.dbias;
     if (dst == nullptr) return;
     float sum = 0.0f;
-    for (int32_t p = 0; p < a.parts; ++p) sum += a.partial[int64_t{p} * 2 * a.cols + i];
-    const int64_t c = i < a.cols ? i : i - a.cols;
+    if (c < a.cols)
+        for (int32_t p = wave; p < a.parts; p += 16) sum += a.partial[(int64_t{p} * 2 + blockIdx.y) * a.cols + c];
+    s[wave][lane] = sum;
+    __syncthreads();
+    if (wave != 0 || c >= a.cols) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) sum += s[i][lane];
     if (a.gdt == FSDPPACK_BF16) static_cast<uint16_t *>(dst)[c] = static_cast<uint16_t>(to_bf16(sum));
     else static_cast<float *>(dst)[c] = sum;
 }
 
 // dg = dh u a'(g), du = dh a(g), and h = a(g) u where it is wanted again.
 // They are rounded to bf16, the type in which the matrix products that follow
-// read them.
-__device__ __forceinline__ void load8_any(const Mat &m, int64_t r, int32_t c, int32_t cols, float *v)
+// read them.  Bound by memory.
+template <int KT, bool FLAT>
+__device__ __forceinline__ void load_kept(const Mat &m, int64_t t, int64_t row, int32_t c, int32_t cols, float *v)
 {
-    const uint8_t *sc = m.scales + r * ((cols + kGroup - 1) / kGroup);
-    if (m.dt == FSDPPACK_BF16) load8<FSDPPACK_BF16>(row_of(m, r), nullptr, c, cols, v);
-    else if (m.dt == FSDPPACK_E4M3) load8<FSDPPACK_E4M3>(row_of(m, r), sc, c, cols, v);
-    else load8<FSDPPACK_INT8>(row_of(m, r), sc, c, cols, v);
+    constexpr int size = KT == FSDPPACK_BF16 ? 2 : 1;
+    if constexpr (FLAT) load8<KT>(static_cast<const char *>(m.p) + t * 8 * size, m.scales + (t >> 2), 0, 8, v);
+    else load8<KT>(row_of(m, row), m.scales + row * ((cols + kGroup - 1) / kGroup), c, cols, v);
 }
 
-__global__ void __launch_bounds__(kThreads) gate_backward_kernel(GateArgs a)
+template <int GT, int UT, bool FLAT>
+__global__ void __launch_bounds__(kThreads) gate_backward_kernel(GateArgs a, Rows w)
 {
-    const int32_t cols = a.cols, units = (cols + 7) / 8;
-    for (int64_t t = int64_t{blockIdx.x} * kThreads + threadIdx.x; t < a.rows * units; t += int64_t{gridDim.x} * kThreads) {
-        const int64_t r = t / units;
-        const int32_t c = static_cast<int32_t>(t - r * units) * 8;
-        float d[8], g[8], u[8], h[8];
-        load8<FSDPPACK_BF16>(row_of(a.dout, r), nullptr, c, cols, d);
-        load8_any(a.gate, r, c, cols, g);
-        load8_any(a.up, r, c, cols, u);
+    constexpr int EACH = 2;
+    const int32_t cols = a.cols;
+    const int64_t base = int64_t{blockIdx.x} * (kThreads * EACH);
+    const int64_t base_row = FLAT ? 0 : base / w.per_row;
+    const uint32_t base_unit = FLAT ? 0 : static_cast<uint32_t>(base - base_row * w.per_row);
+    float d[EACH][8], g[EACH][8], u[EACH][8];
+    int64_t row[EACH];
+    int32_t unit[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        const int32_t local = e * kThreads + threadIdx.x;
+        const int64_t t = base + local;
+        if (t >= w.units) continue;
+        unit_at<FLAT>(w, base, local, base_row, base_unit, row[e], unit[e]);
+        load_kept<FSDPPACK_BF16, FLAT>(a.dout, t, row[e], unit[e] * 8, cols, d[e]);
+        load_kept<GT, FLAT>(a.gate, t, row[e], unit[e] * 8, cols, g[e]);
+        load_kept<UT, FLAT>(a.up, t, row[e], unit[e] * 8, cols, u[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        const int64_t t = base + e * kThreads + threadIdx.x;
+        if (t >= w.units) continue;
+        float h[8], dg[8], du[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float act, dact;
-            activation(a.act, g[i], act, dact);
-            h[i] = act * u[i];
-            g[i] = d[i] * u[i] * dact;
-            u[i] = d[i] * act;
+            activation(a.act, g[e][i], act, dact);
+            h[i] = act * u[e][i];
+            dg[i] = d[e][i] * u[e][i] * dact;
+            du[i] = d[e][i] * act;
         }
-        store8(a.dgate + r * a.ldw, FSDPPACK_BF16, c, cols, g);
-        store8(a.dup + r * a.ldw, FSDPPACK_BF16, c, cols, u);
-        if (a.out.p) store8(row_of_out(a.out, r), FSDPPACK_BF16, c, cols, h);
+        if constexpr (FLAT) {
+            store8(a.dgate + t * 8, FSDPPACK_BF16, 0, 8, dg);
+            store8(a.dup + t * 8, FSDPPACK_BF16, 0, 8, du);
+            if (a.out.p) store8(static_cast<uint16_t *>(a.out.p) + t * 8, FSDPPACK_BF16, 0, 8, h);
+        } else {
+            store8(a.dgate + row[e] * a.ldw, FSDPPACK_BF16, unit[e] * 8, cols, dg);
+            store8(a.dup + row[e] * a.ldw, FSDPPACK_BF16, unit[e] * 8, cols, du);
+            if (a.out.p) store8(row_of_out(a.out, row[e]), FSDPPACK_BF16, unit[e] * 8, cols, h);
+        }
     }
 }
 
@@ -228,6 +569,24 @@ int blocks_for(int64_t work, int64_t per_block)
 {
     return static_cast<int>(std::min<int64_t>((work + per_block - 1) / per_block, 1 << 16));
 }
+
+Rows rows_of(int64_t rows, int64_t per_row)
+{
+    // per_row <= 2^18 and n < per_row + 2^10 < 2^31: with 2^s >= per_row and
+    // m = ceil(2^(31 + s) / per_row) < 2^32, n m / 2^(31 + s) is n / per_row
+    // plus less than n / 2^31 of a unit, which does not reach the next one
+    Rows w;
+    w.units = rows * per_row;
+    w.per_row = static_cast<uint32_t>(per_row);
+    uint32_t s = 0;
+    while ((int64_t{1} << s) < per_row) ++s;
+    const uint64_t p = uint64_t{1} << (31 + s);
+    w.magic = static_cast<uint32_t>((p + per_row - 1) / per_row);
+    w.shift = 31 + s;
+    return w;
+}
+
+bool one_row(const Mat &m, int64_t rows, int64_t cols) { return m.p == nullptr || rows == 1 || m.ld == cols; }
 
 }  // namespace
 
@@ -238,33 +597,95 @@ int blocks_for(int64_t work, int64_t per_block)
 int launch_checkpoint(const Mat &x, const Mat &q, int64_t rows, int64_t cols, bool save, void *stream, void *e0, void *e1)
 {
     const int32_t c = static_cast<int32_t>(cols);
-    const dim3 grid(blocks_for(rows * ((cols + kGroup - 1) / kGroup * 4), kThreads)), block(kThreads);
-    if (save && x.dt == FSDPPACK_BF16) LAUNCH(save_kernel<FSDPPACK_BF16>, grid, block, x, q, rows, c);
-    else if (save) LAUNCH(save_kernel<FSDPPACK_FP32>, grid, block, x, q, rows, c);
-    else if (q.dt == FSDPPACK_E4M3) LAUNCH(load_kernel<FSDPPACK_E4M3>, grid, block, q, x, rows, c);
-    else LAUNCH(load_kernel<FSDPPACK_INT8>, grid, block, q, x, rows, c);
+    const bool flat = cols % kGroup == 0 && one_row(x, rows, cols);
+    // a saved row has whole scale groups of four units
+    const Rows w = rows_of(rows, save ? (cols + kGroup - 1) / kGroup * 4 : (cols + 7) / 8);
+    const dim3 grid(static_cast<uint32_t>((w.units + kSpan - 1) / kSpan)), block(kThreads);
+#define SAVE(XT, QT)                                                                   \
+    if (flat) LAUNCH((save_kernel<XT, QT, true>), grid, block, x, q, w, c);            \
+    else LAUNCH((save_kernel<XT, QT, false>), grid, block, x, q, w, c)
+#define LOAD(QT)                                                                       \
+    if (flat) LAUNCH((load_kernel<QT, true>), grid, block, q, x, w, c);                \
+    else LAUNCH((load_kernel<QT, false>), grid, block, q, x, w, c)
+    if (!save) {
+        if (q.dt == FSDPPACK_E4M3) { LOAD(FSDPPACK_E4M3); } else { LOAD(FSDPPACK_INT8); }
+    } else if (x.dt == FSDPPACK_BF16) {
+        if (q.dt == FSDPPACK_E4M3) { SAVE(FSDPPACK_BF16, FSDPPACK_E4M3); } else { SAVE(FSDPPACK_BF16, FSDPPACK_INT8); }
+    } else {
+        if (q.dt == FSDPPACK_E4M3) { SAVE(FSDPPACK_FP32, FSDPPACK_E4M3); } else { SAVE(FSDPPACK_FP32, FSDPPACK_INT8); }
+    }
+#undef SAVE
+#undef LOAD
     return static_cast<int>(hipGetLastError());
 }
 
 int launch_norm_forward(const NormArgs &a, void *stream, void *e0, void *e1)
 {
-    const dim3 grid(blocks_for(a.rows, 1)), block(kThreads);
-    if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_forward_kernel<FSDPPACK_BF16>, grid, block, a);
-    else LAUNCH(norm_forward_kernel<FSDPPACK_FP32>, grid, block, a);
+    const dim3 loop_grid(blocks_for(a.rows, 1)), block(kThreads);
+    // enough blocks for every CU to hold as many as it can; each keeps its weights over its rows
+#define ROWS(WAVES, NV)                                                                                                    \
+    {                                                                                                                      \
+        constexpr int threads = WAVES > 4 ? 64 * WAVES : kThreads, groups = threads / 64 / WAVES;                          \
+        const dim3 grid(static_cast<uint32_t>(std::min<int64_t>((a.rows + groups - 1) / groups, 256 * 2048 / threads)));   \
+        if (a.x.dt == FSDPPACK_BF16) LAUNCH((norm_forward_rows_kernel<FSDPPACK_BF16, WAVES, NV>), grid, dim3(threads), a); \
+        else LAUNCH((norm_forward_rows_kernel<FSDPPACK_FP32, WAVES, NV>), grid, dim3(threads), a);                         \
+        return static_cast<int>(hipGetLastError());                                                                        \
+    }
+    if (a.cols <= 512) ROWS(1, 1)
+    if (a.cols <= 1024) ROWS(1, 2)
+    if (a.cols <= 2048) ROWS(4, 1)
+    if (a.cols <= 4096) ROWS(4, 2)
+    if (a.cols <= 8192) ROWS(8, 2)
+    if (a.cols <= 16384) ROWS(16, 2)
+#undef ROWS
+    if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_forward_kernel<FSDPPACK_BF16>, loop_grid, block, a);
+    else LAUNCH(norm_forward_kernel<FSDPPACK_FP32>, loop_grid, block, a);
     return static_cast<int>(hipGetLastError());
 }
 
+// Partial sums of the weight's gradient: one per block, as many blocks as the
+// card holds; rows too long for registers are dealt out over up to 512 parts.
+namespace {
+constexpr int kBackThreads = 512;
+int row_waves(int64_t cols) { return cols <= 1024 ? 1 : cols <= 4096 ? 4 : cols <= 8192 ? 8 : 16; }
+int back_threads(int64_t cols) { return std::max(kBackThreads, 64 * row_waves(cols)); }
+}  // namespace
+
 int norm_backward_parts(int64_t rows, int64_t cols)
 {
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 512)));
+    if (cols > 16384) return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 512)));
+    const int groups = back_threads(cols) / 64 / row_waves(cols);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, 512)));
 }
 
-int launch_norm_backward(const NormBackArgs &a, void *stream, void *e0, void *end, int *launches)
+int launch_norm_backward(const NormBackArgs &args, void *stream, void *e0, void *end, int *launches)
 {
-    const bool sums = a.dweight != nullptr || a.dbias != nullptr;
+    NormBackArgs a = args;
+    const bool sums = a.dweight != nullptr || a.dbias != nullptr, in_registers = a.cols <= 16384;
+    if (!sums) a.partial = nullptr;
     void *e1 = sums ? nullptr : end;
     *launches = 0;
-    if (a.rows > 0) {
+    if (a.rows > 0 && in_registers) {
+        const dim3 grid(a.parts);
+#define ROWS(WAVES, NV)                                                                                                       \
+    {                                                                                                                         \
+        constexpr int threads = WAVES > 8 ? 64 * WAVES : kBackThreads;                                                        \
+        const dim3 block(threads);                                                                                            \
+        if (a.x.dt == FSDPPACK_BF16) LAUNCH((norm_backward_rows_kernel<FSDPPACK_BF16, WAVES, NV, threads>), grid, block, a);  \
+        else if (a.x.dt == FSDPPACK_FP32) LAUNCH((norm_backward_rows_kernel<FSDPPACK_FP32, WAVES, NV, threads>), grid, block, a); \
+        else if (a.x.dt == FSDPPACK_E4M3) LAUNCH((norm_backward_rows_kernel<FSDPPACK_E4M3, WAVES, NV, threads>), grid, block, a); \
+        else LAUNCH((norm_backward_rows_kernel<FSDPPACK_INT8, WAVES, NV, threads>), grid, block, a);                          \
+    }
+        if (a.cols <= 512) ROWS(1, 1)
+        else if (a.cols <= 1024) ROWS(1, 2)
+        else if (a.cols <= 2048) ROWS(4, 1)
+        else if (a.cols <= 4096) ROWS(4, 2)
+        else if (a.cols <= 8192) ROWS(8, 2)
+        else ROWS(16, 2)
+#undef ROWS
+        ++*launches;
+        e0 = nullptr;
+    } else if (a.rows > 0) {
         const dim3 grid(blocks_for(a.rows, 1)), block(kThreads);
         if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_dx_kernel<FSDPPACK_BF16>, grid, block, a);
         else if (a.x.dt == FSDPPACK_FP32) LAUNCH(norm_dx_kernel<FSDPPACK_FP32>, grid, block, a);
@@ -274,23 +695,40 @@ int launch_norm_backward(const NormBackArgs &a, void *stream, void *e0, void *en
         e0 = nullptr;
     }
     if (sums) {
-        const dim3 grid((a.cols + 511) / 512, a.parts), block(64);
-        if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_dw_kernel<FSDPPACK_BF16>, grid, block, a);
-        else if (a.x.dt == FSDPPACK_FP32) LAUNCH(norm_dw_kernel<FSDPPACK_FP32>, grid, block, a);
-        else if (a.x.dt == FSDPPACK_E4M3) LAUNCH(norm_dw_kernel<FSDPPACK_E4M3>, grid, block, a);
-        else LAUNCH(norm_dw_kernel<FSDPPACK_INT8>, grid, block, a);
-        e0 = nullptr;
+        if (!in_registers || a.rows == 0) {           // no rows: the parts are zero
+            const dim3 grid((a.cols + 511) / 512, a.parts), block(64);
+            if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_dw_kernel<FSDPPACK_BF16>, grid, block, a);
+            else if (a.x.dt == FSDPPACK_FP32) LAUNCH(norm_dw_kernel<FSDPPACK_FP32>, grid, block, a);
+            else if (a.x.dt == FSDPPACK_E4M3) LAUNCH(norm_dw_kernel<FSDPPACK_E4M3>, grid, block, a);
+            else LAUNCH(norm_dw_kernel<FSDPPACK_INT8>, grid, block, a);
+            ++*launches;
+        }
+        e0 = *launches ? nullptr : e0;
         e1 = end;
-        LAUNCH(norm_join_kernel, dim3((2 * a.cols + kThreads - 1) / kThreads), dim3(kThreads), a);
-        *launches += 2;
+        LAUNCH(norm_join_kernel, dim3((a.cols + 63) / 64, 2), dim3(1024), a);
+        ++*launches;
     }
     return static_cast<int>(hipGetLastError());
 }
 
 int launch_gate_backward(const GateArgs &a, void *stream, void *e0, void *e1)
 {
-    const dim3 grid(blocks_for(a.rows * ((a.cols + 7) / 8), kThreads)), block(kThreads);
-    LAUNCH(gate_backward_kernel, grid, block, a);
+    const bool flat = a.cols % kGroup == 0 && a.ldw == a.cols && one_row(a.dout, a.rows, a.cols) && one_row(a.gate, a.rows, a.cols) &&
+                      one_row(a.up, a.rows, a.cols) && one_row(a.out, a.rows, a.cols);
+    const Rows w = rows_of(a.rows, (a.cols + 7) / 8);
+    const dim3 grid(static_cast<uint32_t>((w.units + 2 * kThreads - 1) / (2 * kThreads))), block(kThreads);
+#define GATE(GT, UT)                                                            \
+    if (flat) LAUNCH((gate_backward_kernel<GT, UT, true>), grid, block, a, w);  \
+    else LAUNCH((gate_backward_kernel<GT, UT, false>), grid, block, a, w)
+#define GATE_UP(GT)                                                             \
+    if (a.up.dt == FSDPPACK_BF16) { GATE(GT, FSDPPACK_BF16); }                  \
+    else if (a.up.dt == FSDPPACK_E4M3) { GATE(GT, FSDPPACK_E4M3); }             \
+    else { GATE(GT, FSDPPACK_INT8); }
+    if (a.gate.dt == FSDPPACK_BF16) { GATE_UP(FSDPPACK_BF16) }
+    else if (a.gate.dt == FSDPPACK_E4M3) { GATE_UP(FSDPPACK_E4M3) }
+    else { GATE_UP(FSDPPACK_INT8) }
+#undef GATE_UP
+#undef GATE
     return static_cast<int>(hipGetLastError());
 }
 
