@@ -26,8 +26,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int BK = 64;               // reduction elements per step
 constexpr int kXcds = 8;             // workgroups go round-robin over 8 dies, each with its own L2
@@ -296,12 +294,21 @@ template <int DT>
 __device__ __forceinline__ void keep_row8(const Mat &o, int64_t j, int64_t col, int64_t cols, bool row_ok, const float *v)
 {
     const int h = (threadIdx.x >> 5) & 1;
-    float top = fmaxf(top_of8(v), top_of8(v + 8));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const int e = scale_exponent<DT>(top);
+    uint32_t bits = max(top_bits8(v), top_bits8(v + 8));
+    bits = max(bits, static_cast<uint32_t>(__shfl_xor(static_cast<int>(bits), 32)));
     uint32_t w[4];
-    encode8<DT>(v, e, w[0], w[1]);
-    encode8<DT>(v + 8, e, w[2], w[3]);
+    int e;
+    if (bits < kLastPlain) {
+        e = scale_exponent<DT>(__uint_as_float(bits));
+        encode8<DT, true>(v, e, w[0], w[1]);
+        encode8<DT, true>(v + 8, e, w[2], w[3]);
+    } else {                              // both lanes of the group
+        float top = fmaxf(finite_top8(v), finite_top8(v + 8));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        e = scale_exponent<DT>(top);
+        encode8<DT, false>(v, e, w[0], w[1]);
+        encode8<DT, false>(v + 8, e, w[2], w[3]);
+    }
     // dword q: columns 8 q + 4 h; lanes below 32 get columns 0..15, the others 16..31
     const u32x4 b = join_halves(u32x2{w[0], w[1]}, u32x2{w[2], w[3]});
     if (!row_ok) return;

@@ -34,6 +34,7 @@ struct NormArgs {
     float *stats;                     // [rows, 2]: mean, 1 / standard deviation
     int64_t rows;
     int32_t cols, wdt, rms;
+    int32_t stream;                   // store past the caches
     float eps;
 };
 
@@ -45,6 +46,7 @@ struct NormBackArgs {
     float *partial;                   // [parts, 2, cols] sums of dy * xh and dy
     int64_t rows;
     int32_t cols, wdt, gdt, rms, parts;
+    int32_t stream;
 };
 
 struct GateArgs {                     // elementwise part of the gated block's backward pass

@@ -11,8 +11,6 @@
 namespace fsdppack {
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kThreads = 256;
 
 // Where a thread's units of `SIZE` columns lie.  FLAT: rows follow one another
@@ -25,8 +23,7 @@ struct Rows {
 };
 
 template <bool FLAT>
-__device__ __forceinline__ void unit_at(const Rows &w, int64_t base, int32_t local, int64_t base_row, uint32_t base_unit, int64_t &row,
-                                        int32_t &unit)
+__device__ __forceinline__ void unit_at(const Rows &w, int32_t local, int64_t base_row, uint32_t base_unit, int64_t &row, int32_t &unit)
 {
     if constexpr (FLAT) {
         row = 0;
@@ -39,67 +36,73 @@ __device__ __forceinline__ void unit_at(const Rows &w, int64_t base, int32_t loc
     }
 }
 
-// A block takes kSpan units in a row, kEach of every thread's; its first unit's
-// row is found once.
-constexpr int kEach = 4, kSpan = kThreads * kEach;
+// A block takes kSpan units in a row, kEach of every thread's, all loads before
+// the first store; its first unit's row is found once.  Two units a thread
+// measured 6.0 TB/s (save, 8192 x 12288), one 5.7, four 5.8.
+constexpr int kEach = 2, kSpan = kThreads * kEach;
 
 template <int XT, int QT, bool FLAT>
-__global__ void __launch_bounds__(kThreads) save_kernel(Mat x, Mat q, Rows w, int32_t cols)
+__global__ void __launch_bounds__(kThreads) save_kernel(Mat x, Mat q, Rows w, int32_t cols, bool stream)
 {
     const int64_t base = int64_t{blockIdx.x} * kSpan;
     const int64_t base_row = FLAT ? 0 : base / w.per_row;
     const uint32_t base_unit = FLAT ? 0 : static_cast<uint32_t>(base - base_row * w.per_row);
-    float v[kEach][8];
+    const int32_t left = w.units - base < kSpan ? static_cast<int32_t>(w.units - base) : kSpan;
+    constexpr int SIZE = XT == FSDPPACK_BF16 ? 2 : 4;
+    Raw8<XT> raw[kEach];
     int64_t row[kEach];
     int32_t unit[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
         const int32_t local = e * kThreads + threadIdx.x;
-        const int64_t t = base + local;
-        if (t >= w.units) continue;
-        unit_at<FLAT>(w, base, local, base_row, base_unit, row[e], unit[e]);
-        if constexpr (FLAT) load8<XT>(static_cast<const char *>(x.p) + t * (XT == FSDPPACK_BF16 ? 16 : 32), nullptr, 0, 8, v[e]);
-        else load8<XT>(row_of(x, row[e]), nullptr, unit[e] * 8, cols, v[e]);
+        if (local >= left) continue;
+        unit_at<FLAT>(w, local, base_row, base_unit, row[e], unit[e]);
+        if constexpr (FLAT) raw[e] = read8<XT>(static_cast<const char *>(x.p) + base * 8 * SIZE, nullptr, local * 8, kSpan * 8);
+        else raw[e] = read8<XT>(row_of(x, row[e]), nullptr, unit[e] * 8, cols);
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const int64_t t = base + e * kThreads + threadIdx.x;
-        if (t >= w.units) continue;       // the same for the four threads of a group
+        const int32_t local = e * kThreads + threadIdx.x;
+        if (local >= left) continue;      // the same for the four threads of a group
+        float v[8];
+        value8<XT>(raw[e], v);
         uint8_t *p = static_cast<uint8_t *>(q.p);
         if constexpr (FLAT) {
-            save8_as<QT>(p + (t >> 2) * kGroup, q.scales + (t >> 2), static_cast<int32_t>(t & 3) * 8, kGroup, v[e]);
+            save8_as<QT>(p + base * 8, q.scales + (base >> 2), local * 8, kSpan * 8, v, stream);
         } else {
             const int32_t groups = (cols + kGroup - 1) / kGroup;
-            save8_as<QT>(p + row[e] * q.ld, q.scales + row[e] * groups, unit[e] * 8, cols, v[e]);
+            save8_as<QT>(p + row[e] * q.ld, q.scales + row[e] * groups, unit[e] * 8, cols, v, false);
         }
     }
 }
 
 template <int QT, bool FLAT>
-__global__ void __launch_bounds__(kThreads) load_kernel(Mat q, Mat out, Rows w, int32_t cols)
+__global__ void __launch_bounds__(kThreads) load_kernel(Mat q, Mat out, Rows w, int32_t cols, bool stream)
 {
     const int64_t base = int64_t{blockIdx.x} * kSpan;
     const int64_t base_row = FLAT ? 0 : base / w.per_row;
     const uint32_t base_unit = FLAT ? 0 : static_cast<uint32_t>(base - base_row * w.per_row);
-    float v[kEach][8];
+    const int32_t left = w.units - base < kSpan ? static_cast<int32_t>(w.units - base) : kSpan;
+    Raw8<QT> raw[kEach];
     int64_t row[kEach];
     int32_t unit[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
         const int32_t local = e * kThreads + threadIdx.x;
-        const int64_t t = base + local;
-        if (t >= w.units) continue;
-        unit_at<FLAT>(w, base, local, base_row, base_unit, row[e], unit[e]);
-        if constexpr (FLAT) load8<QT>(static_cast<const char *>(q.p) + t * 8, q.scales + (t >> 2), 0, 8, v[e]);
-        else load8<QT>(row_of(q, row[e]), q.scales + row[e] * ((cols + kGroup - 1) / kGroup), unit[e] * 8, cols, v[e]);
+        if (local >= left) continue;
+        unit_at<FLAT>(w, local, base_row, base_unit, row[e], unit[e]);
+        if constexpr (FLAT) raw[e] = read8<QT>(static_cast<const char *>(q.p) + base * 8, q.scales + (base >> 2), local * 8, kSpan * 8);
+        else raw[e] = read8<QT>(row_of(q, row[e]), q.scales + row[e] * ((cols + kGroup - 1) / kGroup), unit[e] * 8, cols);
     }
     const int32_t size = out.dt == FSDPPACK_BF16 ? 16 : 32;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const int64_t t = base + e * kThreads + threadIdx.x;
-        if (t >= w.units) continue;
-        if constexpr (FLAT) store8(static_cast<char *>(out.p) + t * size, out.dt, 0, 8, v[e]);
-        else store8(row_of_out(out, row[e]), out.dt, unit[e] * 8, cols, v[e]);
+        const int32_t local = e * kThreads + threadIdx.x;
+        if (local >= left) continue;
+        float v[8];
+        value8<QT>(raw[e], v);
+        if constexpr (FLAT) store8(static_cast<char *>(out.p) + base * size, out.dt, local * 8, kSpan * 8, v, stream);
+        else store8(row_of_out(out, row[e]), out.dt, unit[e] * 8, cols, v);
     }
 }
 
@@ -140,17 +143,32 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float *s)
 }
 
 // A row in the registers of WAVES wavefronts, NV units of 8 columns a lane:
-// read once from memory, next row's loads under way while this one is summed.
-// Bound by memory.  A block of THREADS works on THREADS / 64 / WAVES rows at a
-// time and keeps the weights of its columns for all of its rows.
-template <int XT, int WAVES, int NV>
-__global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) norm_forward_rows_kernel(NormArgs a)
+// read once from memory, the next row's loads under way while this one is
+// summed.  Bound by memory: one unit a lane (NV = 1) up to 8192 columns, since
+// registers decide how many rows a CU has in flight.  A block of THREADS works
+// on THREADS / 64 / WAVES rows at a time and keeps the weights of its columns
+// for all of its rows.
+// Six wavefronts a SIMD (80 registers) and just the blocks that then fit: 25.5
+// us at 8192 x 4096 against 28.2 without the limit, 33.0 with eight.
+template <int XT, int WAVES, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(WAVES < 16 ? 6 : 4))) norm_forward_rows_kernel(NormArgs a)
 {
-    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : kThreads, GROUPS = THREADS / 64 / WAVES;
-    __shared__ float s[2][2][GROUPS * WAVES];
+    constexpr int GROUPS = THREADS / 64 / WAVES;
+    __shared__ float s[2][2 * GROUPS * WAVES];
     const int32_t cols = a.cols;
-    const int lane = threadIdx.x % (64 * WAVES);
-    float w[NV][8], b[NV][8], v[NV][8], next[NV][8];
+    const int lane = threadIdx.x % (64 * WAVES), wave = __builtin_amdgcn_readfirstlane(lane >> 6);
+    float w[NV][8], b[NV][8], v[NV][8];
+    // columns of the row in a wavefront's lanes
+    auto count = [&](int i) {
+        int32_t n = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t left = cols - (i + k * WAVES) * 512;
+            n += left < 0 ? 0 : left < 512 ? left : 512;
+        }
+        return n;
+    };
+    Raw8<XT> next[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int32_t c = (lane + k * 64 * WAVES) * 8;
@@ -158,43 +176,69 @@ __global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) norm_forwar
         load_weight(a.bias, a.wdt, c, cols, 0.0f, b[k]);
     }
     const int64_t step = int64_t{gridDim.x} * GROUPS;
-    int64_t r = int64_t{blockIdx.x} * GROUPS + threadIdx.x / (64 * WAVES);
+    int64_t r = int64_t{blockIdx.x} * GROUPS + __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * WAVES));
     auto read = [&](int64_t row) {
         const void *x = row_of(a.x, row < a.rows ? row : a.rows - 1);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) load8<XT>(x, nullptr, (lane + k * 64 * WAVES) * 8, cols, next[k]);
+        for (int k = 0; k < NV; ++k) next[k] = read8<XT>(x, nullptr, (lane + k * 64 * WAVES) * 8, cols);
     };
     const float inv = 1.0f / static_cast<float>(cols);
+    const float my_inv = count(wave) > 0 ? 1.0f / static_cast<float>(count(wave)) : 0.0f;
     read(r);
     // the same number of turns for all of a block's wavefronts (they meet in row_sums)
     for (int64_t first = int64_t{blockIdx.x} * GROUPS, turn = 0; first < a.rows; first += step, r += step, ++turn) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = next[k][i];
+        for (int k = 0; k < NV; ++k) value8<XT>(next[k], v[k]);
         if (first + step < a.rows) read(r + step);
-        float mean = 0.0f;
+        // LayerNorm: each wavefront's own mean and spread about it, joined as
+        // means of samples of count[w] values are, so that the wavefronts
+        // meet once and nothing cancels
+        float mean = 0.0f, own = 0.0f;
         if (!a.rms) {
-            float sum[1] = {0.0f};
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[0] += v[k][i];
-            row_sums<WAVES>(sum, s[0][turn & 1]);
-            mean = sum[0] * inv;
+                for (int i = 0; i < 8; ++i) own += v[k][i];
+            own = wave_sum(own) * my_inv;
         }
-        float sq[1] = {0.0f};
+        float sq = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int32_t c = (lane + k * 64 * WAVES) * 8;
+            float d[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = c + i < cols ? v[k][i] - mean : 0.0f;
-                sq[0] += d * d;
+            for (int i = 0; i < 8; ++i) d[i] = v[k][i] - own;
+            if (c + 8 > cols)             // the row's end
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = c + i < cols ? d[i] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sq += d[i] * d[i];
+        }
+        sq = wave_sum(sq);
+        mean = own;
+        if constexpr (WAVES > 1) {
+            float *mine = s[turn & 1] + threadIdx.x / (64 * WAVES) * (2 * WAVES);
+            if ((threadIdx.x & 63) == 0) {
+                mine[wave] = own;
+                mine[WAVES + wave] = sq;
+            }
+            __syncthreads();
+            sq = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WAVES; ++i) sq += mine[WAVES + i];
+            if (!a.rms) {
+                mean = 0.0f;
+#pragma unroll
+                for (int i = 0; i < WAVES; ++i) mean += mine[i] * static_cast<float>(count(i));
+                mean *= inv;
+#pragma unroll
+                for (int i = 0; i < WAVES; ++i) {
+                    const float d = mine[i] - mean;
+                    sq += d * d * static_cast<float>(count(i));
+                }
             }
         }
-        row_sums<WAVES>(sq, s[1][turn & 1]);
-        const float rstd = 1.0f / sqrtf(sq[0] * inv + a.eps);
+        const float rstd = 1.0f / sqrtf(sq * inv + a.eps);
         if (r >= a.rows) continue;
         if (lane == 0) {
             a.stats[2 * r] = mean;
@@ -206,10 +250,13 @@ __global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) norm_forwar
             if (c >= (cols + kGroup - 1) / kGroup * kGroup) continue;     // by whole groups of four lanes
             float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = c + i < cols ? (v[k][i] - mean) * rstd * w[k][i] + b[k][i] : 0.0f;
-            store8(row_of_out(a.out, r), a.out.dt, c, cols, y);
-            if (a.x_ckpt.p) save8(a.x_ckpt, r, c, cols, v[k]);
-            if (a.out_ckpt.p) save8(a.out_ckpt, r, c, cols, y);
+            for (int i = 0; i < 8; ++i) y[i] = (v[k][i] - mean) * rstd * w[k][i] + b[k][i];
+            if (c + 8 > cols)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = c + i < cols ? y[i] : 0.0f;
+            store8(row_of_out(a.out, r), a.out.dt, c, cols, y, a.stream);
+            if (a.x_ckpt.p) save8(a.x_ckpt, r, c, cols, v[k], a.stream);
+            if (a.out_ckpt.p) save8(a.out_ckpt, r, c, cols, y, a.stream);
         }
     }
 }
@@ -279,105 +326,57 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(NormArgs a)
 // lies in the registers of WAVES wavefronts; each lane also sums dy xh and dy
 // of its columns over the block's rows, and the block writes one partial sum a
 // column.  THREADS are many (512), so that few partial sums are written.
-template <int XT, int WAVES, int NV, int THREADS>
+template <int XT, int DT, int WAVES, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_backward_rows_kernel(NormBackArgs a)
 {
-    constexpr bool AHEAD = THREADS <= 512;       // 1024 threads have no registers for the next row's bits
     constexpr int GROUPS = THREADS / 64 / WAVES;
-    constexpr bool EIGHT = XT == FSDPPACK_E4M3 || XT == FSDPPACK_INT8;
     __shared__ float s[2][2 * GROUPS * WAVES];
-    __shared__ float joined[GROUPS > 1 ? 64 * WAVES * 8 : 1];
+    __shared__ float joined[GROUPS > 1 ? THREADS * 8 : 1];
     const int32_t cols = a.cols, groups = (cols + kGroup - 1) / kGroup;
-    const int lane = threadIdx.x % (64 * WAVES), group = threadIdx.x / (64 * WAVES);
+    const int lane = threadIdx.x % (64 * WAVES), group = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * WAVES));
     float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
-    u32x4 nx[NV][XT == FSDPPACK_FP32 ? 2 : 1], nd[NV][2];
-    uint32_t nsc[NV] = {};
+    Raw8<XT> nx[NV];
+    Raw8<DT> nd[NV];
+    float2 nst;
 #pragma unroll
     for (int k = 0; k < NV; ++k) load_weight(a.weight, a.wdt, (lane + k * 64 * WAVES) * 8, cols, 1.0f, w[k]);
     const float inv = 1.0f / static_cast<float>(cols);
-    const bool wide_d = a.dout.dt == FSDPPACK_FP32;
-    // the bits of 8 elements from column c on; zeros past the row's end
-    auto bits = [&](const char *row, int size, int32_t c, u32x4 *o) {
-        const int32_t n = cols - c;
-        const char *p = row + int64_t{c} * size;
-        typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(2)));
-        if (size == 1) {
-            u32x2u q = {0, 0};
-            if (n >= 8) q = *reinterpret_cast<const u32x2u *>(p);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < n) q[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i & 3));
-            o[0] = u32x4{q.x, q.y, 0, 0};
-        } else if (size == 2) {
-            o[0] = u32x4{0, 0, 0, 0};
-            if (n >= 8) {
-                const u32x4b q = *reinterpret_cast<const u32x4b *>(p);
-                o[0] = u32x4{q.x, q.y, q.z, q.w};
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < n) o[0][i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << (16 * (i & 1));
-            }
-        } else {
-            o[0] = o[1] = u32x4{0, 0, 0, 0};
-            if (n >= 8) {
-                const u32x4b q = *reinterpret_cast<const u32x4b *>(p), t = *reinterpret_cast<const u32x4b *>(p + 16);
-                o[0] = u32x4{q.x, q.y, q.z, q.w};
-                o[1] = u32x4{t.x, t.y, t.z, t.w};
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < n) o[i >> 2][i & 3] = reinterpret_cast<const uint32_t *>(p)[i];
-            }
-        }
-    };
-    auto values = [](const u32x4 *o, bool wide, float *v) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = wide ? __uint_as_float(o[i >> 2][i & 3]) : (i & 1) ? bf16_hi(o[0][i >> 1]) : bf16_lo(o[0][i >> 1]);
-    };
-    float2 nst = {0.0f, 0.0f};
     auto read = [&](int64_t row) {
         row = row < a.rows ? row : a.rows - 1;
-        const char *x = static_cast<const char *>(row_of(a.x, row)), *d = static_cast<const char *>(row_of(a.dout, row));
+        const void *x = row_of(a.x, row), *d = row_of(a.dout, row);
         nst = float2{a.stats[2 * row], a.stats[2 * row + 1]};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int32_t c = (lane + k * 64 * WAVES) * 8;
-            bits(x, XT == FSDPPACK_FP32 ? 4 : XT == FSDPPACK_BF16 ? 2 : 1, c, nx[k]);
-            if constexpr (EIGHT) nsc[k] = c < cols ? a.x.scales[row * groups + c / kGroup] : 0;
-            if (wide_d) bits(d, 4, c, nd[k]);
-            else bits(d, 2, c, nd[k]);
+            nx[k] = read8<XT>(x, a.x.scales + row * groups, c, cols);
+            nd[k] = read8<DT>(d, nullptr, c, cols);
         }
     };
     const int64_t step = int64_t{gridDim.x} * GROUPS;
     int64_t r = int64_t{blockIdx.x} * GROUPS + group;
-    if (AHEAD) read(r);
+    read(r);
     for (int64_t first = int64_t{blockIdx.x} * GROUPS, turn = 0; first < a.rows; first += step, r += step, ++turn) {
-        if (!AHEAD) read(r);
-        // xh and dy of the row; nothing of a row that is not there
+        // xh and dy of the row (dy is 0 past its end); nothing of a row that is not there
         float xh[NV][8], d[NV][8];
-        const float mean = nst.x, rstd = nst.y;
         const bool there = r < a.rows;
+        const float mean = there ? nst.x : 0.0f, rstd = there ? nst.y : 0.0f;
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int32_t c = (lane + k * 64 * WAVES) * 8;
-            if constexpr (EIGHT) decode8<XT>(nx[k][0].x, nx[k][0].y, __uint_as_float(nsc[k] << 23), xh[k]);
-            else values(nx[k], XT == FSDPPACK_FP32, xh[k]);
-            values(nd[k], wide_d, d[k]);
+            value8<XT>(nx[k], xh[k]);
+            value8<DT>(nd[k], d[k]);
+            if (!there)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xh[k][i] = d[k][i] = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool in = there && c + i < cols;
-                xh[k][i] = in ? (xh[k][i] - mean) * rstd : 0.0f;
-                d[k][i] = in ? d[k][i] : 0.0f;
+                xh[k][i] = (xh[k][i] - mean) * rstd;
                 const float t = d[k][i] * w[k][i];
                 sum[0] += t * xh[k][i];
                 sum[1] += t;
             }
         }
-        if (AHEAD && first + step < a.rows) read(r + step);
+        if (first + step < a.rows) read(r + step);
         row_sums<WAVES>(sum, s[turn & 1]);
         const float c2 = sum[0] * inv, c1 = a.rms ? 0.0f : sum[1] * inv;
 #pragma unroll
@@ -390,38 +389,40 @@ __global__ void __launch_bounds__(THREADS) norm_backward_rows_kernel(NormBackArg
                 dw[k][i] += d[k][i] * xh[k][i];
                 db[k][i] += d[k][i];
             }
-            if (there) store8(row_of_out(a.dx, r), a.dx.dt, c, cols, o);
+            if (there) store8(row_of_out(a.dx, r), a.dx.dt, c, cols, o, a.stream);
         }
     }
     if (a.partial == nullptr) return;
-    // the groups' sums, one after the other
+    // one partial sum a column and block: the groups' sums in order
     float *p = a.partial + int64_t{blockIdx.x} * 2 * cols;
 #pragma unroll
-    for (int which = 0; which < 2; ++which)
+    for (int which = 0; which < 2; ++which) {
+        if (which == 1 && a.dbias == nullptr) break;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int32_t c = (lane + k * 64 * WAVES) * 8;
             float *v = which ? db[k] : dw[k];
             if constexpr (GROUPS > 1) {
-#pragma unroll 1
-                for (int from = 0; from < GROUPS; ++from) {
-                    if (group == from) {
+                constexpr int PER = 64 * WAVES * 8;      // columns of a group
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float *at = &joined[i * 64 * WAVES + lane];
-                            *at = from == 0 ? v[i] : *at + v[i];
-                        }
-                    }
-                    __syncthreads();
-                }
-                if (group == 0) {
+                for (int i = 0; i < 8; ++i) joined[group * PER + i * 64 * WAVES + lane] = v[i];
+                __syncthreads();
+                // each thread one eighth of a unit's columns (GROUPS = 8), a quarter, ...
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = joined[i * 64 * WAVES + lane];
+                for (int i = 0; i < 8 / GROUPS; ++i) {
+                    const int at = (group * (8 / GROUPS) + i) * 64 * WAVES + lane;
+                    float t = joined[at];
+#pragma unroll
+                    for (int g = 1; g < GROUPS; ++g) t += joined[g * PER + at];
+                    const int32_t col = c + group * (8 / GROUPS) + i;
+                    if (col < cols) p[which * cols + col] = t;
                 }
                 __syncthreads();
+            } else {
+                store8(p + which * cols, FSDPPACK_FP32, c, cols, v);
             }
-            if (group == 0) store8(p + which * cols, FSDPPACK_FP32, c, cols, v);
         }
+    }
 }
 
 // Rows too long for registers: dx alone, the row read twice.
@@ -497,8 +498,19 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(NormBackArgs a)
     void *dst = blockIdx.y == 0 ? a.dweight : a.dbias;
     if (dst == nullptr) return;
     float sum = 0.0f;
-    if (c < a.cols)
-        for (int32_t p = wave; p < a.parts; p += 16) sum += a.partial[(int64_t{p} * 2 + blockIdx.y) * a.cols + c];
+    if (c < a.cols) {
+        // eight loads at a time: their latency is what this kernel would wait for
+        const float *p = a.partial + (int64_t{wave} * 2 + blockIdx.y) * a.cols + c;
+        const int64_t pitch = int64_t{32} * a.cols;
+        int32_t n = (a.parts - wave + 15) / 16;
+        for (; n >= 8; n -= 8, p += 8 * pitch) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = p[i * pitch];
+            sum += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+        }
+        for (; n > 0; --n, p += pitch) sum += *p;
+    }
     s[wave][lane] = sum;
     __syncthreads();
     if (wave != 0 || c >= a.cols) return;
@@ -512,11 +524,11 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(NormBackArgs a)
 // They are rounded to bf16, the type in which the matrix products that follow
 // read them.  Bound by memory.
 template <int KT, bool FLAT>
-__device__ __forceinline__ void load_kept(const Mat &m, int64_t t, int64_t row, int32_t c, int32_t cols, float *v)
+__device__ __forceinline__ Raw8<KT> read_kept(const Mat &m, int64_t base, int32_t local, int64_t row, int32_t c, int32_t cols)
 {
     constexpr int size = KT == FSDPPACK_BF16 ? 2 : 1;
-    if constexpr (FLAT) load8<KT>(static_cast<const char *>(m.p) + t * 8 * size, m.scales + (t >> 2), 0, 8, v);
-    else load8<KT>(row_of(m, row), m.scales + row * ((cols + kGroup - 1) / kGroup), c, cols, v);
+    if constexpr (FLAT) return read8<KT>(static_cast<const char *>(m.p) + base * 8 * size, m.scales + (base >> 2), local * 8, 1 << 30);
+    else return read8<KT>(row_of(m, row), m.scales + row * ((cols + kGroup - 1) / kGroup), c, cols);
 }
 
 template <int GT, int UT, bool FLAT>
@@ -527,39 +539,44 @@ __global__ void __launch_bounds__(kThreads) gate_backward_kernel(GateArgs a, Row
     const int64_t base = int64_t{blockIdx.x} * (kThreads * EACH);
     const int64_t base_row = FLAT ? 0 : base / w.per_row;
     const uint32_t base_unit = FLAT ? 0 : static_cast<uint32_t>(base - base_row * w.per_row);
-    float d[EACH][8], g[EACH][8], u[EACH][8];
+    const int32_t left = w.units - base < kThreads * EACH ? static_cast<int32_t>(w.units - base) : kThreads * EACH;
+    Raw8<FSDPPACK_BF16> rd[EACH];
+    Raw8<GT> rg[EACH];
+    Raw8<UT> ru[EACH];
     int64_t row[EACH];
     int32_t unit[EACH];
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
         const int32_t local = e * kThreads + threadIdx.x;
-        const int64_t t = base + local;
-        if (t >= w.units) continue;
-        unit_at<FLAT>(w, base, local, base_row, base_unit, row[e], unit[e]);
-        load_kept<FSDPPACK_BF16, FLAT>(a.dout, t, row[e], unit[e] * 8, cols, d[e]);
-        load_kept<GT, FLAT>(a.gate, t, row[e], unit[e] * 8, cols, g[e]);
-        load_kept<UT, FLAT>(a.up, t, row[e], unit[e] * 8, cols, u[e]);
+        if (local >= left) continue;
+        unit_at<FLAT>(w, local, base_row, base_unit, row[e], unit[e]);
+        rd[e] = read_kept<FSDPPACK_BF16, FLAT>(a.dout, base, local, row[e], unit[e] * 8, cols);
+        rg[e] = read_kept<GT, FLAT>(a.gate, base, local, row[e], unit[e] * 8, cols);
+        ru[e] = read_kept<UT, FLAT>(a.up, base, local, row[e], unit[e] * 8, cols);
     }
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
-        const int64_t t = base + e * kThreads + threadIdx.x;
-        if (t >= w.units) continue;
-        float h[8], dg[8], du[8];
+        const int32_t local = e * kThreads + threadIdx.x;
+        if (local >= left) continue;
+        float d[8], g[8], u[8], h[8];
+        value8<FSDPPACK_BF16>(rd[e], d);
+        value8<GT>(rg[e], g);
+        value8<UT>(ru[e], u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float act, dact;
-            activation(a.act, g[e][i], act, dact);
-            h[i] = act * u[e][i];
-            dg[i] = d[e][i] * u[e][i] * dact;
-            du[i] = d[e][i] * act;
+            activation(a.act, g[i], act, dact);
+            h[i] = act * u[i];
+            g[i] = d[i] * u[i] * dact;
+            u[i] = d[i] * act;
         }
         if constexpr (FLAT) {
-            store8(a.dgate + t * 8, FSDPPACK_BF16, 0, 8, dg);
-            store8(a.dup + t * 8, FSDPPACK_BF16, 0, 8, du);
-            if (a.out.p) store8(static_cast<uint16_t *>(a.out.p) + t * 8, FSDPPACK_BF16, 0, 8, h);
+            store8(a.dgate + base * 8, FSDPPACK_BF16, local * 8, 1 << 30, g);
+            store8(a.dup + base * 8, FSDPPACK_BF16, local * 8, 1 << 30, u);
+            if (a.out.p) store8(static_cast<uint16_t *>(a.out.p) + base * 8, FSDPPACK_BF16, local * 8, 1 << 30, h);
         } else {
-            store8(a.dgate + row[e] * a.ldw, FSDPPACK_BF16, unit[e] * 8, cols, dg);
-            store8(a.dup + row[e] * a.ldw, FSDPPACK_BF16, unit[e] * 8, cols, du);
+            store8(a.dgate + row[e] * a.ldw, FSDPPACK_BF16, unit[e] * 8, cols, g);
+            store8(a.dup + row[e] * a.ldw, FSDPPACK_BF16, unit[e] * 8, cols, u);
             if (a.out.p) store8(row_of_out(a.out, row[e]), FSDPPACK_BF16, unit[e] * 8, cols, h);
         }
     }
@@ -586,6 +603,9 @@ Rows rows_of(int64_t rows, int64_t per_row)
     return w;
 }
 
+// Bytes that a call reads and writes from which on it stores past the caches.
+constexpr int64_t kStreamBytes = int64_t{32} << 20;
+
 bool one_row(const Mat &m, int64_t rows, int64_t cols) { return m.p == nullptr || rows == 1 || m.ld == cols; }
 
 }  // namespace
@@ -598,15 +618,16 @@ int launch_checkpoint(const Mat &x, const Mat &q, int64_t rows, int64_t cols, bo
 {
     const int32_t c = static_cast<int32_t>(cols);
     const bool flat = cols % kGroup == 0 && one_row(x, rows, cols);
+    const bool stream_out = rows * cols * (x.dt == FSDPPACK_BF16 ? 3 : 5) >= kStreamBytes;
     // a saved row has whole scale groups of four units
     const Rows w = rows_of(rows, save ? (cols + kGroup - 1) / kGroup * 4 : (cols + 7) / 8);
     const dim3 grid(static_cast<uint32_t>((w.units + kSpan - 1) / kSpan)), block(kThreads);
 #define SAVE(XT, QT)                                                                   \
-    if (flat) LAUNCH((save_kernel<XT, QT, true>), grid, block, x, q, w, c);            \
-    else LAUNCH((save_kernel<XT, QT, false>), grid, block, x, q, w, c)
+    if (flat) LAUNCH((save_kernel<XT, QT, true>), grid, block, x, q, w, c, stream_out);            \
+    else LAUNCH((save_kernel<XT, QT, false>), grid, block, x, q, w, c, false)
 #define LOAD(QT)                                                                       \
-    if (flat) LAUNCH((load_kernel<QT, true>), grid, block, q, x, w, c);                \
-    else LAUNCH((load_kernel<QT, false>), grid, block, q, x, w, c)
+    if (flat) LAUNCH((load_kernel<QT, true>), grid, block, q, x, w, c, stream_out);                \
+    else LAUNCH((load_kernel<QT, false>), grid, block, q, x, w, c, false)
     if (!save) {
         if (q.dt == FSDPPACK_E4M3) { LOAD(FSDPPACK_E4M3); } else { LOAD(FSDPPACK_INT8); }
     } else if (x.dt == FSDPPACK_BF16) {
@@ -619,72 +640,88 @@ int launch_checkpoint(const Mat &x, const Mat &q, int64_t rows, int64_t cols, bo
     return static_cast<int>(hipGetLastError());
 }
 
-int launch_norm_forward(const NormArgs &a, void *stream, void *e0, void *e1)
+// Up to 16384 columns a row lies in the registers of `waves` wavefronts.
+namespace {
+constexpr int64_t kRowCols = 16384;
+constexpr int row_waves(int64_t cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : cols <= 4096 ? 8 : 16; }
+// forward: as small a block as a row allows; backward: 512 threads at least,
+// so that a block's rows share one partial sum of the weight's gradient
+constexpr int forward_threads(int waves) { return waves > 4 ? 64 * waves : 256; }
+constexpr int backward_threads(int waves) { return waves > 8 ? 64 * waves : 512; }
+}  // namespace
+
+int launch_norm_forward(const NormArgs &args, void *stream, void *e0, void *e1)
 {
-    const dim3 loop_grid(blocks_for(a.rows, 1)), block(kThreads);
-    // enough blocks for every CU to hold as many as it can; each keeps its weights over its rows
-#define ROWS(WAVES, NV)                                                                                                    \
-    {                                                                                                                      \
-        constexpr int threads = WAVES > 4 ? 64 * WAVES : kThreads, groups = threads / 64 / WAVES;                          \
-        const dim3 grid(static_cast<uint32_t>(std::min<int64_t>((a.rows + groups - 1) / groups, 256 * 2048 / threads)));   \
-        if (a.x.dt == FSDPPACK_BF16) LAUNCH((norm_forward_rows_kernel<FSDPPACK_BF16, WAVES, NV>), grid, dim3(threads), a); \
-        else LAUNCH((norm_forward_rows_kernel<FSDPPACK_FP32, WAVES, NV>), grid, dim3(threads), a);                         \
-        return static_cast<int>(hipGetLastError());                                                                        \
+    NormArgs a = args;
+    const int64_t per = (a.x.dt == FSDPPACK_BF16 ? 2 : 4) + (a.out.dt == FSDPPACK_BF16 ? 2 : 4) + (a.x_ckpt.p != nullptr) + (a.out_ckpt.p != nullptr);
+    a.stream = a.rows * a.cols * per >= kStreamBytes;
+    // as many blocks as the CUs hold at once; each keeps its weights over its rows
+#define ROWS(WAVES, NV)                                                                                                          \
+    {                                                                                                                            \
+        constexpr int threads = forward_threads(WAVES), groups = threads / 64 / WAVES;                                           \
+        const dim3 grid(static_cast<uint32_t>(std::min<int64_t>((a.rows + groups - 1) / groups, 256 * (WAVES < 16 ? 1536 : 2048) / threads)));         \
+        if (a.x.dt == FSDPPACK_BF16) LAUNCH((norm_forward_rows_kernel<FSDPPACK_BF16, WAVES, NV, threads>), grid, dim3(threads), a); \
+        else LAUNCH((norm_forward_rows_kernel<FSDPPACK_FP32, WAVES, NV, threads>), grid, dim3(threads), a);                      \
     }
     if (a.cols <= 512) ROWS(1, 1)
-    if (a.cols <= 1024) ROWS(1, 2)
-    if (a.cols <= 2048) ROWS(4, 1)
-    if (a.cols <= 4096) ROWS(4, 2)
-    if (a.cols <= 8192) ROWS(8, 2)
-    if (a.cols <= 16384) ROWS(16, 2)
+    else if (a.cols <= 1024) ROWS(2, 1)
+    else if (a.cols <= 2048) ROWS(4, 1)
+    else if (a.cols <= 4096) ROWS(8, 1)
+    else if (a.cols <= 8192) ROWS(16, 1)
+    else if (a.cols <= kRowCols) ROWS(16, 2)
 #undef ROWS
-    if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_forward_kernel<FSDPPACK_BF16>, loop_grid, block, a);
-    else LAUNCH(norm_forward_kernel<FSDPPACK_FP32>, loop_grid, block, a);
+    else {
+        const dim3 grid(blocks_for(a.rows, 1)), block(kThreads);
+        if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_forward_kernel<FSDPPACK_BF16>, grid, block, a);
+        else LAUNCH(norm_forward_kernel<FSDPPACK_FP32>, grid, block, a);
+    }
     return static_cast<int>(hipGetLastError());
 }
 
-// Partial sums of the weight's gradient: one per block, as many blocks as the
-// card holds; rows too long for registers are dealt out over up to 512 parts.
+// Partial sums of the weight's gradient: one per block, at most kParts blocks;
+// rows too long for registers are dealt out over as many parts.
 namespace {
-constexpr int kBackThreads = 512;
-int row_waves(int64_t cols) { return cols <= 1024 ? 1 : cols <= 4096 ? 4 : cols <= 8192 ? 8 : 16; }
-int back_threads(int64_t cols) { return std::max(kBackThreads, 64 * row_waves(cols)); }
-}  // namespace
+constexpr int kParts = 512;
+}
 
 int norm_backward_parts(int64_t rows, int64_t cols)
 {
-    if (cols > 16384) return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 512)));
-    const int groups = back_threads(cols) / 64 / row_waves(cols);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, 512)));
+    const int waves = row_waves(cols), groups = cols > kRowCols ? 1 : backward_threads(waves) / 64 / waves;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, kParts)));
 }
 
 int launch_norm_backward(const NormBackArgs &args, void *stream, void *e0, void *end, int *launches)
 {
     NormBackArgs a = args;
-    const bool sums = a.dweight != nullptr || a.dbias != nullptr, in_registers = a.cols <= 16384;
+    const bool sums = a.dweight != nullptr || a.dbias != nullptr, in_registers = a.cols <= kRowCols;
+    const int64_t per = (a.x.dt == FSDPPACK_FP32 ? 4 : a.x.dt == FSDPPACK_BF16 ? 2 : 1) + (a.dout.dt == FSDPPACK_BF16 ? 2 : 4) +
+                        (a.dx.dt == FSDPPACK_BF16 ? 2 : 4);
+    a.stream = a.rows * a.cols * per >= kStreamBytes;
     if (!sums) a.partial = nullptr;
     void *e1 = sums ? nullptr : end;
     *launches = 0;
     if (a.rows > 0 && in_registers) {
         const dim3 grid(a.parts);
-#define ROWS(WAVES, NV)                                                                                                       \
-    {                                                                                                                         \
-        constexpr int threads = WAVES > 8 ? 64 * WAVES : kBackThreads;                                                        \
-        const dim3 block(threads);                                                                                            \
-        if (a.x.dt == FSDPPACK_BF16) LAUNCH((norm_backward_rows_kernel<FSDPPACK_BF16, WAVES, NV, threads>), grid, block, a);  \
-        else if (a.x.dt == FSDPPACK_FP32) LAUNCH((norm_backward_rows_kernel<FSDPPACK_FP32, WAVES, NV, threads>), grid, block, a); \
-        else if (a.x.dt == FSDPPACK_E4M3) LAUNCH((norm_backward_rows_kernel<FSDPPACK_E4M3, WAVES, NV, threads>), grid, block, a); \
-        else LAUNCH((norm_backward_rows_kernel<FSDPPACK_INT8, WAVES, NV, threads>), grid, block, a);                          \
+#define ROWS_AS(XT, WAVES, NV)                                                                                                          \
+    if (a.dout.dt == FSDPPACK_BF16) LAUNCH((norm_backward_rows_kernel<XT, FSDPPACK_BF16, WAVES, NV, threads>), grid, dim3(threads), a); \
+    else LAUNCH((norm_backward_rows_kernel<XT, FSDPPACK_FP32, WAVES, NV, threads>), grid, dim3(threads), a);
+#define ROWS(WAVES, NV)                                                          \
+    {                                                                            \
+        constexpr int threads = backward_threads(WAVES);                         \
+        if (a.x.dt == FSDPPACK_BF16) { ROWS_AS(FSDPPACK_BF16, WAVES, NV) }       \
+        else if (a.x.dt == FSDPPACK_FP32) { ROWS_AS(FSDPPACK_FP32, WAVES, NV) }  \
+        else if (a.x.dt == FSDPPACK_E4M3) { ROWS_AS(FSDPPACK_E4M3, WAVES, NV) }  \
+        else { ROWS_AS(FSDPPACK_INT8, WAVES, NV) }                               \
     }
         if (a.cols <= 512) ROWS(1, 1)
-        else if (a.cols <= 1024) ROWS(1, 2)
+        else if (a.cols <= 1024) ROWS(2, 1)
         else if (a.cols <= 2048) ROWS(4, 1)
-        else if (a.cols <= 4096) ROWS(4, 2)
-        else if (a.cols <= 8192) ROWS(8, 2)
+        else if (a.cols <= 4096) ROWS(8, 1)
+        else if (a.cols <= 8192) ROWS(16, 1)
         else ROWS(16, 2)
 #undef ROWS
+#undef ROWS_AS
         ++*launches;
-        e0 = nullptr;
     } else if (a.rows > 0) {
         const dim3 grid(blocks_for(a.rows, 1)), block(kThreads);
         if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_dx_kernel<FSDPPACK_BF16>, grid, block, a);
@@ -692,9 +729,9 @@ int launch_norm_backward(const NormBackArgs &args, void *stream, void *e0, void 
         else if (a.x.dt == FSDPPACK_E4M3) LAUNCH(norm_dx_kernel<FSDPPACK_E4M3>, grid, block, a);
         else LAUNCH(norm_dx_kernel<FSDPPACK_INT8>, grid, block, a);
         ++*launches;
-        e0 = nullptr;
     }
     if (sums) {
+        if (*launches) e0 = nullptr;
         if (!in_registers || a.rows == 0) {           // no rows: the parts are zero
             const dim3 grid((a.cols + 511) / 512, a.parts), block(64);
             if (a.x.dt == FSDPPACK_BF16) LAUNCH(norm_dw_kernel<FSDPPACK_BF16>, grid, block, a);
@@ -702,8 +739,8 @@ int launch_norm_backward(const NormBackArgs &args, void *stream, void *e0, void 
             else if (a.x.dt == FSDPPACK_E4M3) LAUNCH(norm_dw_kernel<FSDPPACK_E4M3>, grid, block, a);
             else LAUNCH(norm_dw_kernel<FSDPPACK_INT8>, grid, block, a);
             ++*launches;
+            e0 = nullptr;
         }
-        e0 = *launches ? nullptr : e0;
         e1 = end;
         LAUNCH(norm_join_kernel, dim3((a.cols + 63) / 64, 2), dim3(1024), a);
         ++*launches;

@@ -81,16 +81,24 @@ def _matrix(m, what: str, dev, eight_bit: bool = False):
     """The C descriptor of a tensor or checkpoint (None for None)."""
     if m is None:
         return None
+    if type(m) is torch.Tensor and m.get_device() == dev and m.is_contiguous():
+        # the usual case in as few steps as it takes; anything else goes on below
+        code = _CODE.get(m.dtype, 0)
+        shape = m.shape
+        if len(shape) == 2 and (code == BF16 or code == FP32):
+            return Matrix(m.data_ptr(), None, shape[0], shape[1], shape[1], code, 0)
     if type(m) is Checkpoint:
         if not eight_bit:
             raise TypeError(f"{what}: expected a torch.Tensor, got a Checkpoint")
         v, s = m.values, m.scales
-        _device(v, f"{what}.values", dev)
-        _device(s, f"{what}.scales", dev)
+        if not isinstance(v, torch.Tensor) or v.get_device() != dev:
+            _device(v, f"{what}.values", dev)
+        if not isinstance(s, torch.Tensor) or s.get_device() != dev:
+            _device(s, f"{what}.scales", dev)
         if v.dim() != 2 or not v.is_contiguous() or v.dtype not in (torch.float8_e4m3fn, torch.int8):
             raise ValueError(f"{what}.values: expected a contiguous 2-D float8_e4m3fn or int8 tensor")
         rows, cols = v.shape
-        if s.dtype is not torch.uint8 or not s.is_contiguous() or tuple(s.shape) != (rows, -(-cols // CHECKPOINT_GROUP)):
+        if s.dtype is not torch.uint8 or not s.is_contiguous() or s.shape != (rows, -(-cols // CHECKPOINT_GROUP)):
             raise ValueError(f"{what}.scales: expected a contiguous uint8 tensor of shape "
                              f"({rows}, {-(-cols // CHECKPOINT_GROUP)})")
         return Matrix(v.data_ptr(), s.data_ptr(), rows, cols, cols, _CODE[v.dtype], 0)
@@ -111,7 +119,8 @@ def _vector(v, what: str, n: int, dev, dtype=None):
     """(pointer, dtype code) of a contiguous vector of n elements."""
     if v is None:
         return None, 0
-    _device(v, what, dev)
+    if type(v) is not torch.Tensor or v.get_device() != dev:
+        _device(v, what, dev)
     code = _CODE.get(v.dtype, 0)
     if (code != BF16 and code != FP32) or (dtype is not None and v.dtype is not dtype):
         raise TypeError(f"{what}: unsupported dtype {v.dtype}")
