@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fsdppack_train_device.h"
@@ -39,6 +40,7 @@ constexpr int kXcds = 8;             // workgroups go round-robin over 8 dies, e
 template <bool TR, int T>
 __device__ __forceinline__ int swizzled(int row, int chunk)
 {
+    static_assert(!TR || T >= 128, "strided tiles have at least 16 chunks a row");
     return TR ? chunk ^ ((row & 3) << 2) : chunk ^ (row >> 1 & 7);
 }
 
@@ -344,7 +346,7 @@ __device__ __forceinline__ void keep_row(const Mat &o, int64_t j, int64_t col, i
 // that neither the barrier nor LDS nor memory latency leaves the matrix cores
 // idle.
 template <GemmKind KIND, int ADT, bool DMA_A, bool DMA_B, int TI, int TJ, int WI, int WJ>
-__global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(GemmArgs g)
+__global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) gemm_kernel(GemmArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)      // the body uses device builtins that the host's pass does not know
     constexpr bool ATR = KIND != kGemmGated, BTR = KIND == kGemmDw;
@@ -517,17 +519,139 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(GemmArgs g)
 #endif
 }
 
-// The splits' partial sums, in a fixed order, rounded once.
+// The gated block for few rows (a token, a short prompt): bound by reading
+// the weights once.  A block has 32 columns of the hidden dimension, their 32
+// rows of W_gate and 32 of W_up; its wavefronts take the reduction 64 elements
+// at a time in turn, straight from memory into the matrix cores' operands (each
+// weight is used once, so LDS would only be in the way), and their sums meet in
+// LDS.  A lane's 16 elements of a step are 32 contiguous bytes: four lanes read
+// a row's whole 128-byte line.  NT: tiles of 16 rows of x.
+constexpr int kFewWaves = 8, kFewRows = 64;
+
+template <int NT>
+__global__ void __launch_bounds__(64 * kFewWaves) gated_few_kernel(GemmArgs g)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    __shared__ float sums[kFewWaves][64][17];            // one tile of rows at a time
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t f0 = int64_t{blockIdx.x} * 32;
+    const int r = lane & 15, q = lane >> 4;
+    // row pointers: weight tile t is rows [16 (t % 2), +16) of matrix t / 2
+    const uint16_t *pw[4], *px[NT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int64_t f = f0 + 16 * (t & 1) + r;
+        const Mat &m = g.a[t >> 1];
+        pw[t] = static_cast<const uint16_t *>(m.p) + (f < g.I ? f : g.I - 1) * m.ld;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int64_t j = 16 * t + r;
+        px[t] = static_cast<const uint16_t *>(g.b[0].p) + (j < g.J ? j : g.J - 1) * g.b[0].ld;
+    }
+    auto chunk = [&](const uint16_t *p, int64_t k) {     // 8 elements from k on, zeros past R
+        u32x4 o = {0, 0, 0, 0};
+        if (k + 8 <= g.R) {
+            const u32x4u w = *reinterpret_cast<const u32x4u *>(p + k);
+            o = u32x4{w.x, w.y, w.z, w.w};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (k + i < g.R) o[i >> 1] |= static_cast<uint32_t>(p[k + i]) << (16 * (i & 1));
+        }
+        return o;
+    };
+    f32x4 acc[4][NT] = {};
+    const int64_t steps = (g.R + 63) / 64;
+    for (int64_t s = wave; s < steps; s += kFewWaves) {
+        const int64_t k = s * 64 + 16 * q;
+        u32x4 w[4][2], x[NT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t][h] = chunk(pw[t], k + 8 * h);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) x[t][h] = chunk(px[t], k + 8 * h);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[t][h]),
+                                                                        __builtin_bit_cast(bf16x8, x[j][h]), acc[t][j], 0, 0, 0);
+    }
+    // lane: row j = lane % 16 of x, weight rows 4 (lane / 16) + 0..3 of the tile
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        if (n) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[wave][16 * t + 4 * q + i][r] = acc[t][n][i];
+        __syncthreads();
+        // four lanes a row of x, 8 columns each: a scale group
+        const int64_t j = 16 * n + (threadIdx.x >> 2);
+        if (threadIdx.x >= 64 || j >= g.J) continue;
+        const int c = static_cast<int>(threadIdx.x & 3) * 8, row = static_cast<int>(threadIdx.x >> 2);
+        float gv[8], uv[8], hv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            gv[i] = uv[i] = 0.0f;
+            if (f0 + c + i < g.I)
+#pragma unroll
+                for (int w = 0; w < kFewWaves; ++w) {
+                    gv[i] += sums[w][c + i][row];
+                    uv[i] += sums[w][32 + c + i][row];
+                }
+            float act, dact;
+            activation(g.act, gv[i], act, dact);
+            hv[i] = act * uv[i];
+        }
+        const int32_t cols = static_cast<int32_t>(g.I), col = static_cast<int32_t>(f0) + c;
+        store8(row_of_out(g.out[0], j), FSDPPACK_BF16, col, cols, hv);
+        auto keep = [&](const Mat &m, const float *v) {
+            if (m.p == nullptr) return;
+            if (m.dt == FSDPPACK_BF16) store8(row_of_out(m, j), FSDPPACK_BF16, col, cols, v);
+            else save8(m, j, col, cols, v);
+        };
+        keep(g.gate, gv);
+        keep(g.up, uv);
+    }
+#endif
+}
+
+// The splits' partial sums, in a fixed order, rounded once.  FLAT: the output
+// has no gaps and whole quads, four elements a thread.
+template <bool FLAT>
 __global__ void __launch_bounds__(256) join_kernel(GemmArgs g)
 {
     const int64_t n = g.J * g.I;
-    for (int64_t t = int64_t{blockIdx.x} * 256 + threadIdx.x; t < n * g.outs; t += int64_t{gridDim.x} * 256) {
-        const int64_t z = t / n, e = t - z * n, j = e / g.I, i = e - j * g.I;
-        float sum = 0.0f;
-        for (int s = 0; s < g.splits; ++s) sum += g.partial[(z * g.splits + s) * n + e];
-        const Mat &o = g.out[z];
-        if (o.dt == FSDPPACK_BF16) static_cast<uint16_t *>(o.p)[j * o.ld + i] = static_cast<uint16_t>(to_bf16(sum));
-        else static_cast<float *>(o.p)[j * o.ld + i] = sum;
+    const int z = blockIdx.y;
+    const float *p = g.partial + int64_t{z} * g.splits * n;
+    const Mat &o = g.out[z];
+    if constexpr (FLAT) {
+        const int64_t at = (int64_t{blockIdx.x} * 256 + threadIdx.x) * 4;
+        if (at >= n) return;
+        f32x4u sum = *reinterpret_cast<const f32x4u *>(p + at);
+#pragma unroll 4
+        for (int s = 1; s < g.splits; ++s) sum += *reinterpret_cast<const f32x4u *>(p + s * n + at);
+        if (o.dt == FSDPPACK_BF16) {
+            typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
+            *reinterpret_cast<u32x2h *>(static_cast<uint16_t *>(o.p) + at) = u32x2h{pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w)};
+        } else {
+            *reinterpret_cast<f32x4u *>(static_cast<float *>(o.p) + at) = sum;
+        }
+    } else {
+        for (int64_t e = int64_t{blockIdx.x} * 256 + threadIdx.x; e < n; e += int64_t{gridDim.x} * 256) {
+            const int64_t j = e / g.I, i = e - j * g.I;
+            float sum = 0.0f;
+            for (int s = 0; s < g.splits; ++s) sum += p[s * n + e];
+            if (o.dt == FSDPPACK_BF16) static_cast<uint16_t *>(o.p)[j * o.ld + i] = static_cast<uint16_t>(to_bf16(sum));
+            else static_cast<float *>(o.p)[j * o.ld + i] = sum;
+        }
     }
 }
 
@@ -537,11 +661,53 @@ __global__ void __launch_bounds__(256) join_kernel(GemmArgs g)
     hipExtLaunchKernelGGL(kernel, grid, block, 0, static_cast<hipStream_t>(stream), static_cast<hipEvent_t>(e0), \
                           static_cast<hipEvent_t>(e1), 0, __VA_ARGS__)
 
-int gemm_splits(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
+namespace {
+
+// How a product is cut: tile and splits of the reduction.
+struct Cut {
+    int tile;                         // 0: 256 x 256, 1: 128 x 128, 2: 128 x 32
+    int splits;
+};
+
+// The cut with the least estimated time.  Blocks run in rounds of as many as
+// the card holds (one, two or three a CU); a round takes a fixed time and one
+// per step, which grows from a CU with one block (and few busy CUs) to a full
+// card; split sums cost a second kernel and their writing and reading.  The
+// figures are microseconds measured on MI355X with each cut forced: 4096 x 512
+// x 2048 takes 76 us as 16 tiles of 256, 43 as 64 of 128, 26 as those in 4
+// splits; 8192 x 4096 x 4096 takes 259 as 256 of 256, 297 as 1024 of 128.
+Cut cut_of(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
 {
-    (void)kind; (void)I; (void)J; (void)R; (void)outs;
-    return 1;
+    constexpr int kTi[3] = {256, 128, 128}, kTj[3] = {256, 128, 32};
+    constexpr double kHeld[3] = {256, 512, 768}, kLone[3] = {128, 256, 256};
+    constexpr double kStepLone[3] = {1.1, 0.6, 0.47}, kStepFull[3] = {2.0, 1.1, 0.9}, kFixed[3] = {8, 3, 2};
+    const int segs = kind == kGemmDx ? 2 : 1;
+    const int64_t steps = (R + BK - 1) / BK * segs;
+    Cut best{0, 1};
+    double least = 1e30;
+    for (int t = 0; t < (kind == kGemmDx ? 3 : 2); ++t) {
+        const int64_t ti = kind == kGemmGated ? kTi[t] / 2 : kTi[t];
+        const int64_t tiles = (I + ti - 1) / ti * ((J + kTj[t] - 1) / kTj[t]) * outs;
+        for (int s = 1; s <= 32; s += s < 4 ? 1 : s < 8 ? 2 : 4) {
+            if (s > 1 && (kind == kGemmGated || steps / s < 4)) break;
+            const double units = static_cast<double>(tiles) * s;
+            const double rounds = std::ceil(units / kHeld[t]);
+            const double full = std::min(1.0, std::max(0.0, (units - kLone[t]) / (kHeld[t] - kLone[t])));
+            const double step = kStepLone[t] + (kStepFull[t] - kStepLone[t]) * full;
+            double us = rounds * (kFixed[t] + step * static_cast<double>((steps + s - 1) / s));
+            if (s > 1) us += 5.0 + 1e-6 * static_cast<double>(I * J) * outs * (2 * s + 1);
+            if (us < least) {
+                least = us;
+                best = Cut{t, s};
+            }
+        }
+    }
+    return best;
 }
+
+}  // namespace
+
+int gemm_splits(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs) { return cut_of(kind, I, J, R, outs).splits; }
 
 namespace {
 
@@ -552,10 +718,9 @@ bool whole_chunks(const Mat &m, int64_t width)
     return m.dt == FSDPPACK_BF16 && reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0 && width % 8 == 0;
 }
 
-template <GemmKind KIND, int ADT, bool DMA_A, bool DMA_B>
-int launch_tiles(GemmArgs &g, void *stream, void *e0, void *e1)
+template <GemmKind KIND, int ADT, bool DMA_A, bool DMA_B, int TI, int TJ, int WI, int WJ>
+int launch_tile(GemmArgs &g, void *stream, void *e0, void *e1)
 {
-    constexpr int TI = 256, TJ = 256, WI = 2, WJ = 4;
     constexpr int step_i = KIND == kGemmGated ? TI / 2 : TI;
     g.tiles_i = static_cast<int32_t>((g.I + step_i - 1) / step_i);
     g.tiles_j = static_cast<int32_t>((g.J + TJ - 1) / TJ);
@@ -563,6 +728,15 @@ int launch_tiles(GemmArgs &g, void *stream, void *e0, void *e1)
     const dim3 grid(static_cast<uint32_t>((tiles + kXcds - 1) / kXcds * kXcds)), block(64 * WI * WJ);
     LAUNCH((gemm_kernel<KIND, ADT, DMA_A, DMA_B, TI, TJ, WI, WJ>), grid, block, g);
     return static_cast<int>(hipGetLastError());
+}
+
+template <GemmKind KIND, int ADT, bool DMA_A, bool DMA_B>
+int launch_tiles(GemmArgs &g, int tile, void *stream, void *e0, void *e1)
+{
+    if (tile == 0) return launch_tile<KIND, ADT, DMA_A, DMA_B, 256, 256, 2, 4>(g, stream, e0, e1);
+    if constexpr (KIND == kGemmDx)
+        if (tile == 2) return launch_tile<KIND, ADT, DMA_A, DMA_B, 128, 32, 4, 1>(g, stream, e0, e1);
+    return launch_tile<KIND, ADT, DMA_A, DMA_B, 128, 128, 2, 2>(g, stream, e0, e1);
 }
 
 }  // namespace
@@ -577,28 +751,40 @@ int launch_gemm(GemmKind kind, GemmArgs g, void *stream, void *e0, void *end, in
     const bool dma = dma_a && dma_b;
     const int adt = g.a[0].dt;
     int rc;
-    if (kind == kGemmGated)
-        rc = dma ? launch_tiles<kGemmGated, FSDPPACK_BF16, true, true>(g, stream, e0, e1)
-                 : launch_tiles<kGemmGated, FSDPPACK_BF16, false, false>(g, stream, e0, e1);
-    else if (kind == kGemmDx)
-        rc = dma ? launch_tiles<kGemmDx, FSDPPACK_BF16, true, true>(g, stream, e0, e1)
-                 : launch_tiles<kGemmDx, FSDPPACK_BF16, false, false>(g, stream, e0, e1);
-    else if (adt == FSDPPACK_BF16)
-        rc = dma ? launch_tiles<kGemmDw, FSDPPACK_BF16, true, true>(g, stream, e0, e1)
-                 : launch_tiles<kGemmDw, FSDPPACK_BF16, false, false>(g, stream, e0, e1);
-    else if (adt == FSDPPACK_E4M3)
-        rc = dma_b ? launch_tiles<kGemmDw, FSDPPACK_E4M3, false, true>(g, stream, e0, e1)
-                   : launch_tiles<kGemmDw, FSDPPACK_E4M3, false, false>(g, stream, e0, e1);
-    else
-        rc = dma_b ? launch_tiles<kGemmDw, FSDPPACK_INT8, false, true>(g, stream, e0, e1)
-                   : launch_tiles<kGemmDw, FSDPPACK_INT8, false, false>(g, stream, e0, e1);
     *launches = 1;
+    if (kind == kGemmGated && g.J <= kFewRows) {
+        const dim3 grid(static_cast<uint32_t>((g.I + 31) / 32)), block(64 * kFewWaves);
+        if (g.J <= 16) LAUNCH(gated_few_kernel<1>, grid, block, g);
+        else if (g.J <= 32) LAUNCH(gated_few_kernel<2>, grid, block, g);
+        else LAUNCH(gated_few_kernel<4>, grid, block, g);
+        return static_cast<int>(hipGetLastError());
+    }
+    const int tile = cut_of(kind, g.I, g.J, g.R, g.outs).tile;
+    if (kind == kGemmGated)
+        rc = dma ? launch_tiles<kGemmGated, FSDPPACK_BF16, true, true>(g, tile, stream, e0, e1)
+                 : launch_tiles<kGemmGated, FSDPPACK_BF16, false, false>(g, tile, stream, e0, e1);
+    else if (kind == kGemmDx)
+        rc = dma ? launch_tiles<kGemmDx, FSDPPACK_BF16, true, true>(g, tile, stream, e0, e1)
+                 : launch_tiles<kGemmDx, FSDPPACK_BF16, false, false>(g, tile, stream, e0, e1);
+    else if (adt == FSDPPACK_BF16)
+        rc = dma ? launch_tiles<kGemmDw, FSDPPACK_BF16, true, true>(g, tile, stream, e0, e1)
+                 : launch_tiles<kGemmDw, FSDPPACK_BF16, false, false>(g, tile, stream, e0, e1);
+    else if (adt == FSDPPACK_E4M3)
+        rc = dma_b ? launch_tiles<kGemmDw, FSDPPACK_E4M3, false, true>(g, tile, stream, e0, e1)
+                   : launch_tiles<kGemmDw, FSDPPACK_E4M3, false, false>(g, tile, stream, e0, e1);
+    else
+        rc = dma_b ? launch_tiles<kGemmDw, FSDPPACK_INT8, false, true>(g, tile, stream, e0, e1)
+                   : launch_tiles<kGemmDw, FSDPPACK_INT8, false, false>(g, tile, stream, e0, e1);
     if (rc != 0) return rc;
     if (g.splits > 1) {
         e0 = nullptr;
         e1 = end;
-        const int64_t n = g.J * g.I * g.outs;
-        LAUNCH(join_kernel, dim3(static_cast<uint32_t>(std::min<int64_t>((n + 255) / 256, 1 << 16))), dim3(256), g);
+        const int64_t n = g.J * g.I;
+        const bool flat = n % 4 == 0 && (g.J == 1 || g.out[0].ld == g.I) && (g.outs == 1 || g.J == 1 || g.out[1].ld == g.I);
+        const int64_t blocks = flat ? (n / 4 + 255) / 256 : std::min<int64_t>((n + 255) / 256, 1 << 16);
+        const dim3 join_grid(static_cast<uint32_t>(blocks), static_cast<uint32_t>(g.outs));
+        if (flat) LAUNCH(join_kernel<true>, join_grid, dim3(256), g);
+        else LAUNCH(join_kernel<false>, join_grid, dim3(256), g);
         ++*launches;
     }
     return static_cast<int>(hipGetLastError());

@@ -137,11 +137,20 @@ int finish(int hip_error, int launches, const char *what)
     return FSDPPACK_OK;
 }
 
-// Every size a product's launch depends on, within the grid's limit.
+// A launch holds fewer than 2^32 work-items; a product takes 256 for 128 x 32
+// elements of its outputs at most (the gated one half as many columns), an
+// elementwise pass one for 16 elements.
 bool product_ok(Check &c, int64_t I, int64_t J, int64_t outs)
 {
-    if ((I + 31) / 32 * ((J + 15) / 16) * outs >= int64_t{1} << 31)
+    if ((I + 63) / 64 * ((J + 31) / 32) * outs >= int64_t{1} << 24)
         return c.fail(FSDPPACK_EINVAL, "the product needs more workgroups than a launch can hold");
+    return true;
+}
+
+bool elements_ok(Check &c, int64_t rows, int64_t cols)
+{
+    if (rows * round_up(cols, kGroup) >= int64_t{1} << 35)
+        return c.fail(FSDPPACK_EINVAL, "the matrix needs more workgroups than a launch can hold");
     return true;
 }
 
@@ -184,7 +193,7 @@ try {
     Check c{"checkpoint_save"};
     Mat mx, mq;
     if (!c.shape(x, "x") || !c.matrix(x, "x", x->rows, x->cols, kDense, &mx) ||
-        !c.matrix(checkpoint, "checkpoint", x->rows, x->cols, kEight, &mq))
+        !c.matrix(checkpoint, "checkpoint", x->rows, x->cols, kEight, &mq) || !elements_ok(c, x->rows, x->cols))
         return c.rc;
     Spans s;
     s.put(mx, x->rows, x->cols, false, "x");
@@ -204,7 +213,8 @@ try {
     Mat mq, mo;
     if (!c.shape(checkpoint, "checkpoint") ||
         !c.matrix(checkpoint, "checkpoint", checkpoint->rows, checkpoint->cols, kEight, &mq) ||
-        !c.matrix(out, "out", checkpoint->rows, checkpoint->cols, kDense, &mo))
+        !c.matrix(out, "out", checkpoint->rows, checkpoint->cols, kDense, &mo) ||
+        !elements_ok(c, checkpoint->rows, checkpoint->cols))
         return c.rc;
     Spans s;
     s.put(mq, checkpoint->rows, checkpoint->cols, false, "checkpoint");
@@ -429,7 +439,7 @@ try {
         !c.matrix(dx, "dx", rows, cols, kDense, &gx.out[0]) || !c.matrix(dw_gate, "dw_gate", ffn, cols, kDense, &gw.out[0]) ||
         !c.matrix(dw_up, "dw_up", ffn, cols, kDense, &gw.out[1]) ||
         (out != nullptr && !c.matrix(out, "out", rows, ffn, kBf16, &e.out)) || !product_ok(c, cols, ffn, 2) ||
-        !product_ok(c, cols, rows, 1))
+        !product_ok(c, cols, rows, 1) || !elements_ok(c, rows, ffn))
         return c.rc;
     const GatedSpace sp = gated_space(rows, ffn, cols);
     if (!workspace_ok(c, workspace, workspace_bytes, sp.bytes)) return c.rc;
