@@ -98,7 +98,7 @@ struct Loader {
     uint32_t scale[DT == FSDPPACK_BF16 ? 1 : kUnits];
 
     // Where the next step's tile starts, and each unit's offset from there in bytes.
-    const char *at, *at2;
+    const char *at, *at2, *next;      // next: the second segment's first step
     const uint8_t *scale_at;
     int64_t pitch, scale_pitch;
     uint32_t off[kUnits], scale_off[DT == FSDPPACK_BF16 ? 1 : kUnits];
@@ -129,6 +129,12 @@ struct Loader {
 #pragma unroll
             for (int c = 0; c < kUnits; ++c) scale_off[c] = (row0 + c * kRows) * groups + col0 / kGroup;
         }
+    }
+
+    // A second segment of the same shape and strides follows.
+    __device__ __forceinline__ void follow(const Mat &m, int64_t t0)
+    {
+        next = static_cast<const char *>(m.p) + (TR ? t0 : t0 * m.ld) * (DT == FSDPPACK_BF16 ? 2 : 1);
     }
 
     // Start bringing in the step at which the loader stands, and go on to the
@@ -251,9 +257,10 @@ __device__ __forceinline__ u32x4 join_halves(u32x2 q0, u32x2 q1)
     return u32x4{x[0], y[0], x[1], y[1]};
 }
 
-// A piece's row (32 columns from `col`, 16 per lane as the matrix cores leave
-// them) as bf16.  Both halves of the wavefront call it.
-__device__ __forceinline__ void store_row(uint16_t *row, int64_t col, int64_t cols, bool row_ok, const float *v)
+// A piece's row (32 columns from `col` of the tile's row, 16 per lane as the
+// matrix cores leave them) as bf16; `cols` of the tile's columns exist.  Both
+// halves of the wavefront call it.
+__device__ __forceinline__ void store_row(uint16_t *row, int col, int cols, bool row_ok, const float *v)
 {
     const int h = (threadIdx.x >> 5) & 1;
 #pragma unroll
@@ -261,30 +268,29 @@ __device__ __forceinline__ void store_row(uint16_t *row, int64_t col, int64_t co
         const float *q = v + 8 * p;
         const u32x4 w = join_halves(u32x2{pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3])},
                                     u32x2{pack_bf16(q[4], q[5]), pack_bf16(q[6], q[7])});
-        const int64_t c = col + 16 * p + 8 * h;
-        if (!row_ok) continue;
+        const int c = col + 16 * p + 8 * h;
+        if (!row_ok || c >= cols) continue;
         if (c + 8 <= cols) {
             *reinterpret_cast<u32x4u *>(row + c) = u32x4u{w.x, w.y, w.z, w.w};
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < cols) row[c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+#pragma unroll 1
+            for (int i = 0; c + i < cols; ++i) row[c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
         }
     }
 }
 
-__device__ __forceinline__ void store_row_fp32(float *row, int64_t col, int64_t cols, bool row_ok, const float *v)
+__device__ __forceinline__ void store_row_fp32(float *row, int col, int cols, bool row_ok, const float *v)
 {
     const int h = (threadIdx.x >> 5) & 1;
     if (!row_ok) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const int64_t c = col + 8 * q + 4 * h;
+        const int c = col + 8 * q + 4 * h;
         if (c + 4 <= cols) {
             *reinterpret_cast<f32x4u *>(row + c) = f32x4u{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 3; ++i)
                 if (c + i < cols) row[c + i] = v[4 * q + i];
         }
     }
@@ -293,7 +299,7 @@ __device__ __forceinline__ void store_row_fp32(float *row, int64_t col, int64_t 
 // A projection's piece kept for the backward pass.  In 8 bits, lanes l and
 // l + 32 hold one scale group (32 columns of a row) between them.
 template <int DT>
-__device__ __forceinline__ void keep_row8(const Mat &o, int64_t j, int64_t col, int64_t cols, bool row_ok, const float *v)
+__device__ __forceinline__ void keep_row8(uint8_t *row, uint8_t *scales, int col, int cols, bool row_ok, const float *v)
 {
     const int h = (threadIdx.x >> 5) & 1;
     uint32_t bits = max(top_bits8(v), top_bits8(v + 8));
@@ -313,28 +319,28 @@ __device__ __forceinline__ void keep_row8(const Mat &o, int64_t j, int64_t col, 
     }
     // dword q: columns 8 q + 4 h; lanes below 32 get columns 0..15, the others 16..31
     const u32x4 b = join_halves(u32x2{w[0], w[1]}, u32x2{w[2], w[3]});
-    if (!row_ok) return;
-    uint8_t *p = static_cast<uint8_t *>(o.p) + j * o.ld;
-    const int64_t c = col + 16 * h;
+    const int c = col + 16 * h;
+    if (!row_ok || c >= cols) return;
     // b = own q0, q1 of the lower lane, then of the upper: columns 0-3, 8-11, 4-7, 12-15
     const uint32_t d[4] = {b.x, b.z, b.y, b.w};
     if (c + 16 <= cols) {
         typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
-        *reinterpret_cast<u32x4b *>(p + c) = u32x4b{d[0], d[1], d[2], d[3]};
+        *reinterpret_cast<u32x4b *>(row + c) = u32x4b{d[0], d[1], d[2], d[3]};
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (c + i < cols) p[c + i] = static_cast<uint8_t>(d[i >> 2] >> (8 * (i & 3)));
+        for (int i = 0; i < 15; ++i)
+            if (c + i < cols) row[c + i] = static_cast<uint8_t>(d[i >> 2] >> (8 * (i & 3)));
     }
-    if (h == 0 && col < cols) o.scales[j * ((cols + kGroup - 1) / kGroup) + col / kGroup] = static_cast<uint8_t>(e + 127);
+    if (h == 0) scales[col / kGroup] = static_cast<uint8_t>(e + 127);
 }
 
-__device__ __forceinline__ void keep_row(const Mat &o, int64_t j, int64_t col, int64_t cols, bool row_ok, const float *v)
+__device__ __forceinline__ void keep_row(const Mat &o, int64_t j, int64_t i0, int64_t I, int col, int cols, bool row_ok, const float *v)
 {
     if (o.p == nullptr) return;
-    if (o.dt == FSDPPACK_BF16) store_row(static_cast<uint16_t *>(o.p) + j * o.ld, col, cols, row_ok, v);
-    else if (o.dt == FSDPPACK_E4M3) keep_row8<FSDPPACK_E4M3>(o, j, col, cols, row_ok, v);
-    else keep_row8<FSDPPACK_INT8>(o, j, col, cols, row_ok, v);
+    if (o.dt == FSDPPACK_BF16) return store_row(static_cast<uint16_t *>(o.p) + j * o.ld + i0, col, cols, row_ok, v);
+    uint8_t *row = static_cast<uint8_t *>(o.p) + j * o.ld + i0, *scales = o.scales + j * ((I + kGroup - 1) / kGroup) + i0 / kGroup;
+    if (o.dt == FSDPPACK_E4M3) keep_row8<FSDPPACK_E4M3>(row, scales, col, cols, row_ok, v);
+    else keep_row8<FSDPPACK_INT8>(row, scales, col, cols, row_ok, v);
 }
 
 // One TI x TJ output tile per block of WI x WJ wavefronts.
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
     __shared__ __align__(1024) uint16_t sa0[TI * BK], sb0[TJ * BK], sa1[TI * BK], sb1[TJ * BK];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    // each die takes a contiguous run of tiles, in bands of 8 tile rows of
+    // each die takes a contiguous run of tiles, in bands of 4 tile rows of
     // the output, so that its neighbours' operands meet in its L2
     const int64_t per_z = int64_t{g.tiles_i} * g.tiles_j, tiles = per_z * g.splits * g.outs;
     const int64_t run = (tiles + kXcds - 1) / kXcds;
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
     if (blockIdx.x / kXcds >= run || t >= tiles) return;
     const int zs = static_cast<int>(t / per_z), z = zs / g.splits, split = zs % g.splits;
     t -= zs * per_z;
-    constexpr int kBand = 8;
+    constexpr int kBand = 4;
     const int64_t band = t / (int64_t{kBand} * g.tiles_i);
     const int high = static_cast<int>(g.tiles_j - band * kBand < kBand ? g.tiles_j - band * kBand : kBand);
     const int in_band = static_cast<int>(t - band * kBand * g.tiles_i);
@@ -375,23 +381,39 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
 
     Loader<ATR, TI, THREADS, ADT, DMA_A, KIND == kGemmGated> la;
     Loader<BTR, TJ, THREADS, FSDPPACK_BF16, DMA_B, false> lb;
-    const int64_t whole1 = g.R / BK;                    // whole steps of a segment
-    const auto &first_b = g.b[KIND == kGemmDw ? z : 0];
-    // a tile read through registers has all of its rows and columns
+    // Steps that are whole and need nothing but the last one's addresses
+    // carried on (or switched to the other segment's, where the two have the
+    // same strides); through registers, only in tiles of which all exists.
     const bool inside = (DMA_A || i_end - i0 >= (KIND == kGemmGated ? TI / 2 : TI)) && (DMA_B || g.J - j0 >= TJ);
-    // bring in step k; WHOLE: it is a whole step and not a segment's first
-    auto start = [&](auto whole, int64_t k, uint16_t *sa, uint16_t *sb) {
+    const bool alike = KIND != kGemmDx || (g.R % BK == 0 && g.a[0].ld == g.a[1].ld && g.b[0].ld == g.b[1].ld);
+    const int64_t plain_end = inside && alike ? g.R / BK * g.segs - s0 : 0;
+    const Mat &first_b = g.b[KIND == kGemmDw ? z : 0];
+    // Start bringing in A's half of step k, then (later) B's.  WHOLE: k > 0 is
+    // a plain step.
+    auto start_a = [&](auto whole, int64_t k, uint16_t *sa) {
         constexpr bool WHOLE = decltype(whole)::value;
         const int64_t step = s0 + k;
+        if (WHOLE && KIND == kGemmDx) la.at = step == steps1 ? la.next : la.at;
         const int seg = KIND == kGemmDx && step >= steps1;
         const int64_t r0 = (step - seg * steps1) * BK;
-        const Mat &b = KIND == kGemmDw ? first_b : g.b[seg];
         if (!WHOLE && (k == 0 || r0 == 0)) {
             la.seek(g.a[seg], KIND == kGemmGated ? g.a[1] : g.a[seg], i0, r0, i_end);
-            lb.seek(b, b, j0, r0, g.J);
+            if (KIND == kGemmDx) la.follow(g.a[1], i0);
         }
         if constexpr (DMA_A) la.template start_dma<WHOLE>(g.R - r0, sa);
         else la.template start_reg<WHOLE>(g.R - r0, i_end - i0);
+    };
+    auto start_b = [&](auto whole, int64_t k, uint16_t *sb) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const int64_t step = s0 + k;
+        if (WHOLE && KIND == kGemmDx) lb.at = step == steps1 ? lb.next : lb.at;
+        const int seg = KIND == kGemmDx && step >= steps1;
+        const int64_t r0 = (step - seg * steps1) * BK;
+        if (!WHOLE && (k == 0 || r0 == 0)) {
+            const Mat &b = KIND == kGemmDw ? first_b : g.b[seg];
+            lb.seek(b, b, j0, r0, g.J);
+            if (KIND == kGemmDx) lb.follow(g.b[1], j0);
+        }
         if constexpr (DMA_B) lb.template start_dma<WHOLE>(g.R - r0, sb);
         else lb.template start_reg<WHOLE>(g.R - r0, g.J - j0);
     };
@@ -418,14 +440,17 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
             for (int k = 0; k < NB; ++k)
                 acc[m][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[from][m], fb[from][k], acc[m][k], 0, 0, 0);
     };
-    // a slice's LDS reads go between its matrix instructions, not before them
-    auto mix = [&]() {
-        constexpr int reads = NA * (ATR ? 2 : 1) + NB * (BTR ? 2 : 1), mm = NA * NB;
+    // A slice's LDS reads and the loads started with it go between its matrix
+    // instructions, evenly: eight wavefronts that start eight loads each at
+    // once hold up each other, and behind the loads their matrix instructions.
+    auto mix = [&](auto loads_) {
+        constexpr int reads = NA * (ATR ? 2 : 1) + NB * (BTR ? 2 : 1), mm = NA * NB, loads = decltype(loads_)::value;
         constexpr int per = (reads + mm - 1) / mm;
 #pragma unroll
         for (int i = 0; i < mm; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // one matrix instruction,
-            __builtin_amdgcn_sched_group_barrier(0x100, per, 0);    // its share of the LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                              // one matrix instruction,
+            __builtin_amdgcn_sched_group_barrier(0x100, per, 0);                            // its share of the LDS reads
+            if (loads * (i + 1) / mm > loads * i / mm) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // and of the loads
         }
     };
     // every wavefront has its loads in LDS and has read the image that is freed
@@ -433,86 +458,89 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
         __builtin_amdgcn_s_waitcnt(0x0070);          // vmcnt(0) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
     };
-    // step k from image (a, b); the other image receives step k + 1, then this
-    // one k + 2.  WHOLE: both exist, and k + 2 is whole and not a segment's first
+    constexpr std::integral_constant<int, 0> none{};
+    constexpr std::integral_constant<int, DMA_A ? TI * BK / 8 / THREADS : 0> a_loads{};
+    constexpr std::integral_constant<int, DMA_B ? TJ * BK / 8 / THREADS : 0> b_loads{};
+    // Step k from image (a, b); B's half of step k + 1 is started into the
+    // other image, A's half of step k + 2 into this one once it is free.
+    // WHOLE: both exist and are plain.
     auto do_step = [&](auto whole, int64_t k, uint16_t *a, uint16_t *b, uint16_t *na, uint16_t *nb) {
         constexpr bool WHOLE = decltype(whole)::value;
+        if (WHOLE || k + 1 < n) start_b(whole, k + 1, nb);
         read(1, a, b, 1);
         multiply(0);
-        mix();
+        mix(b_loads);
         read(0, a, b, 2);
         multiply(1);
-        mix();
+        mix(none);
         read(1, a, b, 3);
         multiply(0);
-        mix();
+        mix(none);
         if (WHOLE || k + 1 < n) {
             la.put(na);
             lb.put(nb);
         }
         meet();
-        if (WHOLE || k + 2 < n) start(whole, k + 2, a, b);
+        if (WHOLE || k + 2 < n) start_a(whole, k + 2, a);
+        // loads into registers stay here: they are used a step from now
+        if constexpr (!DMA_A || !DMA_B) __builtin_amdgcn_sched_barrier(0x78f);
         if (WHOLE || k + 1 < n) read(0, na, nb, 0);
         multiply(1);
-        mix();
+        mix(a_loads);
     };
     constexpr std::true_type plain{};
     constexpr std::false_type any{};
     if (n > 0) {
-        start(any, 0, sa0, sb0);
+        start_a(any, 0, sa0);
+        start_b(any, 0, sb0);
         la.put(sa0);
         lb.put(sb0);
         meet();
-        if (n > 1) start(any, 1, sa1, sb1);
+        if (n > 1) start_a(any, 1, sa1);
         read(0, sa0, sb0, 0);
-        for (int64_t k = 0; k < n;) {
-            // pairs of steps from here that bring in whole steps of the same segment
-            const int64_t next = s0 + k + 2;
-            const int seg = KIND == kGemmDx && next >= steps1;
-            const int64_t end = seg * steps1 + whole1;
-            int64_t pairs = inside && next > seg * steps1 ? ((end - s0 < n ? end - s0 : n) - (k + 2)) / 2 : 0;
-            for (; pairs > 0; --pairs, k += 2) {
-                do_step(plain, k, sa0, sb0, sa1, sb1);
-                do_step(plain, k + 1, sa1, sb1, sa0, sb0);
-            }
+        int64_t k = 0;
+        for (int64_t pairs = ((plain_end < n ? plain_end : n) - 2) / 2; pairs > 0; --pairs, k += 2) {
+            do_step(plain, k, sa0, sb0, sa1, sb1);
+            do_step(plain, k + 1, sa1, sb1, sa0, sb0);
+        }
+        for (; k < n; k += 2) {
             do_step(any, k, sa0, sb0, sa1, sb1);
-            if (++k < n) do_step(any, k, sa1, sb1, sa0, sb0), ++k;
+            if (k + 1 < n) do_step(any, k + 1, sa1, sb1, sa0, sb0);
         }
     }
 
     // lane: output row j = lane % 32, output columns 8 q + 4 (lane / 32) + 0..3 for q < 4
+    const int cols = static_cast<int>(i_end - i0 < TI ? i_end - i0 : TI);
 #pragma unroll
     for (int m = 0; m < NB; ++m) {
         const int64_t j = j0 + piece_b(m) + (lane & 31);
         const bool row_ok = j < g.J;
         if constexpr (KIND == kGemmGated) {
+            uint16_t *row = static_cast<uint16_t *>(g.out[0].p) + j * g.out[0].ld + i0;
 #pragma unroll
             for (int p = 0; p < NA / 2; ++p) {
-                const int64_t i = i0 + piece_a(p);
                 float gv[16], uv[16], hv[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     gv[e] = acc[p][m][e];
                     uv[e] = acc[p + NA / 2][m][e];
-                    float act, dact;
-                    activation(g.act, gv[e], act, dact);
-                    hv[e] = act * uv[e];
+                    hv[e] = activation_alone(g.act, gv[e]) * uv[e];
                 }
-                store_row(static_cast<uint16_t *>(g.out[0].p) + j * g.out[0].ld, i, g.I, row_ok, hv);
-                keep_row(g.gate, j, i, g.I, row_ok, gv);
-                keep_row(g.up, j, i, g.I, row_ok, uv);
+                store_row(row, piece_a(p), cols, row_ok, hv);
+                keep_row(g.gate, j, i0, g.I, piece_a(p), cols, row_ok, gv);
+                keep_row(g.up, j, i0, g.I, piece_a(p), cols, row_ok, uv);
             }
         } else {
+            const Mat &o = g.out[z];
+            float *part = g.partial + ((int64_t{z} * g.splits + split) * g.J + j) * g.I + i0;
 #pragma unroll
             for (int p = 0; p < NA; ++p) {
-                const int64_t i = i0 + piece_a(p);
                 float v[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = acc[p][m][e];
-                const Mat &o = g.out[z];
-                if (g.splits > 1) store_row_fp32(g.partial + ((int64_t{z} * g.splits + split) * g.J + j) * g.I, i, g.I, row_ok, v);
-                else if (o.dt == FSDPPACK_BF16) store_row(static_cast<uint16_t *>(o.p) + j * o.ld, i, g.I, row_ok, v);
-                else store_row_fp32(static_cast<float *>(o.p) + j * o.ld, i, g.I, row_ok, v);
+                if (g.splits > 1) store_row_fp32(part, piece_a(p), cols, row_ok, v);
+                else if (o.dt == FSDPPACK_BF16) store_row(static_cast<uint16_t *>(o.p) + j * o.ld + i0, piece_a(p), cols, row_ok, v);
+                else store_row_fp32(static_cast<float *>(o.p) + j * o.ld + i0, piece_a(p), cols, row_ok, v);
             }
         }
     }

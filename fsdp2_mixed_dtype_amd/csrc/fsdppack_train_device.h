@@ -349,6 +349,14 @@ __device__ __forceinline__ const void *row_of(const Mat &m, int64_t row)
 }
 __device__ __forceinline__ void *row_of_out(const Mat &m, int64_t row) { return const_cast<void *>(row_of(m, row)); }
 
+// The activation at g (see below).
+__device__ __forceinline__ float activation_alone(int act, float g)
+{
+    if (act == FSDPPACK_SILU) return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+    const float g2 = fminf(g * g, 1e8f);
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-2.0f * 0.7978845608028654f * g * (1.0f + 0.044715f * g2)));
+}
+
 // The activation and its derivative at g.
 //  SILU:      a = g s, a' = s (1 + g (1 - s)), s = 1 / (1 + e^-g)
 //  GELU_TANH: a = g p, a' = p + 2 g p (1 - p) k (1 + 3 c g^2), p = 1 / (1 + e^-2v),
