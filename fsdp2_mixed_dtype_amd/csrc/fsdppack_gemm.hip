@@ -548,29 +548,32 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
 }
 
 // The gated block for few rows (a token, a short prompt): bound by reading
-// the weights once.  A block has 32 columns of the hidden dimension, their 32
-// rows of W_gate and 32 of W_up; its wavefronts take the reduction 64 elements
-// at a time in turn, straight from memory into the matrix cores' operands (each
-// weight is used once, so LDS would only be in the way), and their sums meet in
-// LDS.  A lane's 16 elements of a step are 32 contiguous bytes: four lanes read
-// a row's whole 128-byte line.  NT: tiles of 16 rows of x.
-constexpr int kFewWaves = 8, kFewRows = 64;
+// the weights once.  A block has 16 FT columns of the hidden dimension, their
+// rows of W_gate and of W_up (FT = 1, or 2 where a scale group of 32 columns
+// is kept); its wavefronts take the reduction 64 elements at a time in turn,
+// straight from memory into the matrix cores' operands (each weight is used
+// once, so LDS would only be in the way), two or four steps' loads at once,
+// and their sums meet in LDS.  A lane's 16 elements of a step are 32
+// contiguous bytes: four lanes read a row's whole 128-byte line.  NT: tiles of
+// 16 rows of x.
+constexpr int kFewWaves = 8, kFewRows = 32;
 
-template <int NT>
+template <int NT, int FT>
 __global__ void __launch_bounds__(64 * kFewWaves) gated_few_kernel(GemmArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     typedef float f32x4 __attribute__((ext_vector_type(4)));
-    __shared__ float sums[kFewWaves][64][17];            // one tile of rows at a time
+    constexpr int FB = 16 * FT, TILES = 2 * FT, AHEAD = NT == 1 && FT == 1 ? 4 : 2;
+    __shared__ float sums[kFewWaves][2 * FB][17];        // one tile of rows at a time
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t f0 = int64_t{blockIdx.x} * 32;
+    const int64_t f0 = int64_t{blockIdx.x} * FB;
     const int r = lane & 15, q = lane >> 4;
-    // row pointers: weight tile t is rows [16 (t % 2), +16) of matrix t / 2
-    const uint16_t *pw[4], *px[NT];
+    // row pointers: weight tile t is rows [16 (t % FT), +16) of matrix t / FT
+    const uint16_t *pw[TILES], *px[NT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int64_t f = f0 + 16 * (t & 1) + r;
-        const Mat &m = g.a[t >> 1];
+    for (int t = 0; t < TILES; ++t) {
+        const int64_t f = f0 + 16 * (t % FT) + r;
+        const Mat &m = g.a[t / FT];
         pw[t] = static_cast<const uint16_t *>(m.p) + (f < g.I ? f : g.I - 1) * m.ld;
     }
 #pragma unroll
@@ -578,71 +581,101 @@ __global__ void __launch_bounds__(64 * kFewWaves) gated_few_kernel(GemmArgs g)
         const int64_t j = 16 * t + r;
         px[t] = static_cast<const uint16_t *>(g.b[0].p) + (j < g.J ? j : g.J - 1) * g.b[0].ld;
     }
-    auto chunk = [&](const uint16_t *p, int64_t k) {     // 8 elements from k on, zeros past R
+    const int R = static_cast<int>(g.R);
+    auto chunk = [&](const uint16_t *p, int k) {         // 8 elements from k on, zeros past R
         u32x4 o = {0, 0, 0, 0};
-        if (k + 8 <= g.R) {
+        if (k + 8 <= R) {
             const u32x4u w = *reinterpret_cast<const u32x4u *>(p + k);
             o = u32x4{w.x, w.y, w.z, w.w};
         } else {
+#pragma unroll 1
+            for (int i = 0; k + i < R; ++i) {
+                const uint32_t v = static_cast<uint32_t>(p[k + i]) << (16 * (i & 1));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k + i < g.R) o[i >> 1] |= static_cast<uint32_t>(p[k + i]) << (16 * (i & 1));
+                for (int d = 0; d < 4; ++d) o[d] |= i >> 1 == d ? v : 0u;
+            }
         }
         return o;
     };
-    f32x4 acc[4][NT] = {};
-    const int64_t steps = (g.R + 63) / 64;
-    for (int64_t s = wave; s < steps; s += kFewWaves) {
-        const int64_t k = s * 64 + 16 * q;
-        u32x4 w[4][2], x[NT][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) w[t][h] = chunk(pw[t], k + 8 * h);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) x[t][h] = chunk(px[t], k + 8 * h);
-        }
+    f32x4 acc[TILES][NT] = {};
+    u32x4 w[AHEAD][TILES][2], x[AHEAD][NT][2];
+    auto multiply = [&](int n) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < TILES; ++t)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[t][h]),
-                                                                        __builtin_bit_cast(bf16x8, x[j][h]), acc[t][j], 0, 0, 0);
+                    acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[n][t][h]),
+                                                                        __builtin_bit_cast(bf16x8, x[n][j][h]), acc[t][j], 0, 0, 0);
+    };
+    const int steps = (R + 63) / 64;
+    int s = wave;
+    // whole steps, AHEAD at a time: no lane's chunk reaches past the end
+    for (; (s + (AHEAD - 1) * kFewWaves + 1) * 64 <= R; s += AHEAD * kFewWaves) {
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) {
+            const int k = (s + n * kFewWaves) * 64 + 16 * q;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    const u32x4u v = *reinterpret_cast<const u32x4u *>(pw[t] + k + 8 * h);
+                    w[n][t][h] = u32x4{v.x, v.y, v.z, v.w};
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const u32x4u v = *reinterpret_cast<const u32x4u *>(px[t] + k + 8 * h);
+                    x[n][t][h] = u32x4{v.x, v.y, v.z, v.w};
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);               // all loads before the first product waits
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) multiply(n);
+    }
+    for (; s < steps; s += kFewWaves) {
+        const int k = s * 64 + 16 * q;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) w[0][t][h] = chunk(pw[t], k + 8 * h);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) x[0][t][h] = chunk(px[t], k + 8 * h);
+        }
+        multiply(0);
     }
     // lane: row j = lane % 16 of x, weight rows 4 (lane / 16) + 0..3 of the tile
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if (n) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sums[wave][16 * t + 4 * q + i][r] = acc[t][n][i];
         __syncthreads();
-        // four lanes a row of x, 8 columns each: a scale group
-        const int64_t j = 16 * n + (threadIdx.x >> 2);
-        if (threadIdx.x >= 64 || j >= g.J) continue;
-        const int c = static_cast<int>(threadIdx.x & 3) * 8, row = static_cast<int>(threadIdx.x >> 2);
+        // 2 FT lanes a row of x, 8 columns each: a scale group where FT = 2
+        constexpr int PER = 2 * FT;
+        const int row = static_cast<int>(threadIdx.x) / PER, c = static_cast<int>(threadIdx.x) % PER * 8;
+        const int64_t j = 16 * n + row;
+        if (row >= 16 || j >= g.J) continue;
         float gv[8], uv[8], hv[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             gv[i] = uv[i] = 0.0f;
             if (f0 + c + i < g.I)
 #pragma unroll
-                for (int w = 0; w < kFewWaves; ++w) {
-                    gv[i] += sums[w][c + i][row];
-                    uv[i] += sums[w][32 + c + i][row];
+                for (int v = 0; v < kFewWaves; ++v) {
+                    gv[i] += sums[v][c + i][row];
+                    uv[i] += sums[v][FB + c + i][row];
                 }
-            float act, dact;
-            activation(g.act, gv[i], act, dact);
-            hv[i] = act * uv[i];
+            hv[i] = activation_alone(g.act, gv[i]) * uv[i];
         }
         const int32_t cols = static_cast<int32_t>(g.I), col = static_cast<int32_t>(f0) + c;
         store8(row_of_out(g.out[0], j), FSDPPACK_BF16, col, cols, hv);
         auto keep = [&](const Mat &m, const float *v) {
             if (m.p == nullptr) return;
-            if (m.dt == FSDPPACK_BF16) store8(row_of_out(m, j), FSDPPACK_BF16, col, cols, v);
+            if (FT == 1 || m.dt == FSDPPACK_BF16) store8(row_of_out(m, j), FSDPPACK_BF16, col, cols, v);
             else save8(m, j, col, cols, v);
         };
         keep(g.gate, gv);
@@ -706,9 +739,8 @@ struct Cut {
 // splits; 8192 x 4096 x 4096 takes 259 as 256 of 256, 297 as 1024 of 128.
 Cut cut_of(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
 {
-    constexpr int kTi[3] = {256, 128, 128}, kTj[3] = {256, 128, 32};
-    constexpr double kHeld[3] = {256, 512, 768}, kLone[3] = {128, 256, 256};
-    constexpr double kStepLone[3] = {1.1, 0.6, 0.47}, kStepFull[3] = {2.0, 1.1, 0.9}, kFixed[3] = {8, 3, 2};
+    constexpr int kTi[3] = {256, 128, 128}, kTj[3] = {256, 128, 32}, kHeld[3] = {1, 2, 3};
+    constexpr double kStep[3][3] = {{2.0, 0, 0}, {0.62, 1.1, 0}, {0.48, 0.65, 0.9}}, kFixed[3] = {8, 4, 3};
     const int segs = kind == kGemmDx ? 2 : 1;
     const int64_t steps = (R + BK - 1) / BK * segs;
     Cut best{0, 1};
@@ -718,12 +750,13 @@ Cut cut_of(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
         const int64_t tiles = (I + ti - 1) / ti * ((J + kTj[t] - 1) / kTj[t]) * outs;
         for (int s = 1; s <= 32; s += s < 4 ? 1 : s < 8 ? 2 : 4) {
             if (s > 1 && (kind == kGemmGated || steps / s < 4)) break;
-            const double units = static_cast<double>(tiles) * s;
-            const double rounds = std::ceil(units / kHeld[t]);
-            const double full = std::min(1.0, std::max(0.0, (units - kLone[t]) / (kHeld[t] - kLone[t])));
-            const double step = kStepLone[t] + (kStepFull[t] - kStepLone[t]) * full;
-            double us = rounds * (kFixed[t] + step * static_cast<double>((steps + s - 1) / s));
-            if (s > 1) us += 5.0 + 1e-6 * static_cast<double>(I * J) * outs * (2 * s + 1);
+            const int64_t units = tiles * s, held = int64_t{kHeld[t]} * 256;
+            const int64_t rounds = (units + held - 1) / held;
+            const int each = static_cast<int>((std::min(units, held) + 255) / 256);      // blocks on the fullest CU
+            double step = kStep[t][each - 1];
+            if (t == 0 && units < 256) step = 1.1 + 0.9 * static_cast<double>(units) / 256.0;   // half-empty, the clock is higher
+            double us = static_cast<double>(rounds) * (kFixed[t] + step * static_cast<double>((steps + s - 1) / s));
+            if (s > 1) us += 4.0 + 1e-6 * static_cast<double>(I * J) * outs * (0.7 * s + 0.5);
             if (us < least) {
                 least = us;
                 best = Cut{t, s};
@@ -781,10 +814,13 @@ int launch_gemm(GemmKind kind, GemmArgs g, void *stream, void *e0, void *end, in
     int rc;
     *launches = 1;
     if (kind == kGemmGated && g.J <= kFewRows) {
-        const dim3 grid(static_cast<uint32_t>((g.I + 31) / 32)), block(64 * kFewWaves);
-        if (g.J <= 16) LAUNCH(gated_few_kernel<1>, grid, block, g);
-        else if (g.J <= 32) LAUNCH(gated_few_kernel<2>, grid, block, g);
-        else LAUNCH(gated_few_kernel<4>, grid, block, g);
+        const bool groups = (g.gate.p != nullptr && g.gate.dt != FSDPPACK_BF16) || (g.up.p != nullptr && g.up.dt != FSDPPACK_BF16);
+        const int fb = groups ? 32 : 16;
+        const dim3 grid(static_cast<uint32_t>((g.I + fb - 1) / fb)), block(64 * kFewWaves);
+        if (g.J <= 16 && !groups) LAUNCH((gated_few_kernel<1, 1>), grid, block, g);
+        else if (g.J <= 16) LAUNCH((gated_few_kernel<1, 2>), grid, block, g);
+        else if (!groups) LAUNCH((gated_few_kernel<2, 1>), grid, block, g);
+        else LAUNCH((gated_few_kernel<2, 2>), grid, block, g);
         return static_cast<int>(hipGetLastError());
     }
     const int tile = cut_of(kind, g.I, g.J, g.R, g.outs).tile;
