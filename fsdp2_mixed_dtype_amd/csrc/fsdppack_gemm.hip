@@ -44,9 +44,7 @@ __device__ __forceinline__ int swizzled(int row, int chunk)
     return TR ? chunk ^ ((row & 3) << 2) : chunk ^ (row >> 1 & 7);
 }
 
-// Eight codes as bf16, exactly.  E4M3: the hardware's scaled conversion.
-// INT8: code + 128 is an unsigned byte u, and u * scale - 128 * scale is exact
-// in one fused step; u = 0 stands for "not finite".
+// Eight codes as bf16, exactly (E4M3: the hardware's scaled conversion).
 template <int DT>
 __device__ __forceinline__ u32x4 decode8_bf16(uint32_t lo, uint32_t hi, float scale)
 {
@@ -57,12 +55,11 @@ __device__ __forceinline__ u32x4 decode8_bf16(uint32_t lo, uint32_t hi, float sc
         o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
         o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
     } else {
-        const uint32_t a = lo ^ 0x80808080u, b = hi ^ 0x80808080u;
-        const float off = -128.0f * scale;
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(static_cast<float>(((i < 4 ? a : b) >> (8 * (i & 3))) & 0xffu), scale, off);
-        // a zero byte is the code -128
+        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)))) * scale;
+        // a zero byte of these is the code -128
+        const uint32_t a = lo ^ 0x80808080u, b = hi ^ 0x80808080u;
         if ((((a - 0x01010101u) & ~a) | ((b - 0x01010101u) & ~b)) & 0x80808080u) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -305,8 +305,8 @@ int fsdppack_reduce_scatter_copy_out_all(const fsdppack_plan *plan, int32_t rank
  *    *_workspace call gives for the same sizes, aligned to 16, contents
  *    neither read before written nor kept.  Calls that overlap on the GPU
  *    need workspaces of their own; calls ordered on one stream may share one.
- *  - Everything runs on `stream`, allocates nothing and waits for nothing, so
- *    every call may be captured into a graph.  Pointers are read at the call:
+ *  - Everything runs on `stream`, on the current device, allocates nothing and
+ *    waits for nothing, so every call may be captured into a graph.  Pointers are read at the call:
  *    a replay uses the buffers of the captured call.
  *  - A call may launch several kernels (stated with each); timing events set
  *    by fsdppack_time_next_launch are stamped at the start of its first and
@@ -315,13 +315,18 @@ int fsdppack_reduce_scatter_copy_out_all(const fsdppack_plan *plan, int32_t rank
  *    rounded to its dtype once, to nearest even.  Sums are added in an order
  *    fixed by the sizes: the same inputs give the same bits.
  *  - NaN and infinity go through as the formulas have it.
+ *  - A matrix or product that needs more than 2^32 work-items of a launch is
+ *    refused (EINVAL): 2^35 elements for the elementwise passes, 2^24 blocks of
+ *    64 x 32 outputs for a product.
  */
 
 /* A dense or 8-bit matrix.  dtype: FSDPPACK_BF16 or FSDPPACK_FP32 (scales
  * unused), or an activation checkpoint: FSDPPACK_E4M3 or FSDPPACK_INT8, one
  * byte an element, rows contiguous (stride = cols), and `scales` a
  * [rows, ceil(cols / 32)] byte array: element (r, c) stands for
- * code(r, c) * 2^(scales[r][c / 32] - 127). */
+ * code(r, c) * 2^(scales[r][c / 32] - 127).  A checkpoint that
+ * fsdppack_checkpoint_save or norm_forward did not write needs scale bytes of
+ * 17 to 249 (2^-110 to 2^122), as theirs are. */
 typedef struct fsdppack_matrix {
     void *data;
     void *scales;

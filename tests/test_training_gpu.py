@@ -373,6 +373,20 @@ def test_weight_grad_non_finite():
         assert torch.equal(dw[:, keep], torch.full((40, 70), 100.0, device="cuda"))
 
 
+@pytest.mark.parametrize("fmt", EIGHT)
+@pytest.mark.parametrize("top", [3.0e38, 1.0e38, 2.0 ** 121, 2.0 ** -100])
+def test_weight_grad_largest_and_smallest_scales(fmt, top):
+    """Powers of two times small integers: every code and sum is exact."""
+    g = gen(3)
+    k = 2.0 ** math.floor(math.log2(top) - 3)
+    x = (torch.randint(-7, 8, (64, 96), generator=g, device="cuda").double() * k).to(BF)
+    x[0, :] = 7 * k
+    dy = (integers(g, 64, 40).double() * 2.0 ** (-40 if top > 1 else 40)).to(BF)
+    dw = torch.empty(40, 96, device="cuda")
+    fp.weight_grad(dy, save(x, fmt), dw, workspace(fp.weight_grad_workspace(64, 40, 96)))
+    assert torch.equal(dw.double(), dy.double().t().contiguous() @ x.double())
+
+
 def test_weight_grad_offsets_past_32_bits():
     rows, outs, cols = 1 << 19, 4104, 64             # dout: 2.15e9 elements
     dy = torch.zeros(rows, outs, dtype=BF, device="cuda")
@@ -462,14 +476,15 @@ def backward_reference(dy, x, wg, wu, G, Up, act):
 
 @pytest.mark.parametrize("act", [fp.SILU, fp.GELU_TANH])
 @pytest.mark.parametrize("rows,cols,ffn", GATED + [(2055, 512, 264), (0, 40, 72)])
-@pytest.mark.parametrize("kept,x_kind,gdt", [(BF, BF, BF), (fp.E4M3, fp.E4M3, F32), (fp.INT8, BF, F32), (BF, fp.INT8, F32)])
+@pytest.mark.parametrize("kept,x_kind,gdt", [(BF, BF, BF), (fp.E4M3, fp.E4M3, F32), (fp.INT8, BF, F32), (BF, fp.INT8, F32),
+                                             ((BF, fp.E4M3), BF, BF), ((fp.INT8, BF), fp.E4M3, BF), ((fp.E4M3, fp.INT8), BF, F32)])
 def test_gated_backward(act, rows, cols, ffn, kept, x_kind, gdt):
     g = gen(rows * 2 + cols + ffn)
     x, dy = randn(g, rows, cols), randn(g, rows, ffn)
     wg, wu = (randn(g, ffn, cols, std=2 / math.sqrt(cols)) for _ in range(2))
     gate, up = randn(g, rows, ffn, std=2.0), randn(g, rows, ffn)
     ax = x if x_kind is BF else save(x, x_kind)
-    ag, au = (gate, up) if kept is BF else (save(gate, kept), save(up, kept))
+    ag, au = (t if k is BF else save(t, k) for t, k in zip((gate, up), kept if isinstance(kept, tuple) else (kept, kept)))
     see = lambda t: t.double() if isinstance(t, torch.Tensor) else values(t)  # noqa: E731
     dx = torch.full((rows, cols), float("nan"), dtype=gdt, device="cuda")
     dwg, dwu = (torch.full((ffn, cols), float("nan"), dtype=gdt, device="cuda") for _ in range(2))
