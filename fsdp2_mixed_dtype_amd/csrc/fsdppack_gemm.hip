@@ -359,22 +359,24 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
 
     // each die takes a contiguous run of tiles, in bands of 4 tile rows of
     // the output, so that its neighbours' operands meet in its L2
-    const int64_t per_z = int64_t{g.tiles_i} * g.tiles_j, tiles = per_z * g.splits * g.outs;
-    const int64_t run = (tiles + kXcds - 1) / kXcds;
-    int64_t t = blockIdx.x % kXcds * run + blockIdx.x / kXcds;
+    // (fewer than 2^24 tiles: divisions in 32 bits, a few instructions each)
+    const uint32_t per_z = static_cast<uint32_t>(g.tiles_i) * g.tiles_j, tiles = per_z * g.splits * g.outs;
+    const uint32_t run = (tiles + kXcds - 1) / kXcds;
+    uint32_t t = blockIdx.x % kXcds * run + blockIdx.x / kXcds;
     if (blockIdx.x / kXcds >= run || t >= tiles) return;
-    const int zs = static_cast<int>(t / per_z), z = zs / g.splits, split = zs % g.splits;
+    const uint32_t zs = t / per_z;
+    const int z = static_cast<int>(zs / g.splits), split = static_cast<int>(zs - z * g.splits);
     t -= zs * per_z;
-    constexpr int kBand = 4;
-    const int64_t band = t / (int64_t{kBand} * g.tiles_i);
-    const int high = static_cast<int>(g.tiles_j - band * kBand < kBand ? g.tiles_j - band * kBand : kBand);
-    const int in_band = static_cast<int>(t - band * kBand * g.tiles_i);
-    const int64_t tj = band * kBand + in_band % high, ti = in_band / high;
+    constexpr uint32_t kBand = 4;
+    const uint32_t band = t / (kBand * g.tiles_i), in_band = t - band * kBand * g.tiles_i;
+    const uint32_t high = g.tiles_j - band * kBand < kBand ? g.tiles_j - band * kBand : kBand;
+    const int64_t ti = in_band / high, tj = band * kBand + (in_band - static_cast<uint32_t>(ti) * high);
     // the gated product's tile holds TI / 2 rows of W_gate and the same of W_up
     const int64_t i0 = ti * (KIND == kGemmGated ? TI / 2 : TI), j0 = tj * TJ;
     const int64_t i_end = KIND == kGemmGated ? (g.I < i0 + TI / 2 ? g.I : i0 + TI / 2) : g.I;
-    const int64_t steps1 = (g.R + BK - 1) / BK, steps = steps1 * g.segs;
-    const int64_t s0 = steps * split / g.splits, n = steps * (split + 1) / g.splits - s0;
+    const int64_t steps1 = (g.R + BK - 1) / BK;
+    // splits of equal length, the first `longer` of them one step longer
+    const int64_t s0 = g.split_steps * split + (split < g.longer ? split : g.longer), n = g.split_steps + (split < g.longer);
 
     Loader<ATR, TI, THREADS, ADT, DMA_A, KIND == kGemmGated> la;
     Loader<BTR, TJ, THREADS, FSDPPACK_BF16, DMA_B, false> lb;
@@ -767,6 +769,22 @@ Cut cut_of(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
 
 int gemm_splits(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs) { return cut_of(kind, I, J, R, outs).splits; }
 
+// Codes converted on their way into LDS cost the product about 9 % (e4m3) or
+// 25 % (int8) of its time with 256 x 256 tiles and 30 % with 128 x 128, where
+// fewer matrix instructions cover them (8192 x 1024 x 4096: 115 us against
+// 86).  Converted once before, they cost a launch, their reading and twice
+// their writing (15 us for 8192 x 4096), whatever the number of outputs: worth
+// it from a few thousand outputs on.
+bool gemm_reads_converted(int64_t rows, int64_t cols, int64_t outs, int n, int32_t dt)
+{
+    if (dt != FSDPPACK_E4M3 && dt != FSDPPACK_INT8) return false;
+    const double elements = static_cast<double>(rows) * static_cast<double>(cols);
+    const double product_us = 2.0 * elements * static_cast<double>(outs) * n / 1.3e9;
+    const bool big = cut_of(kGemmDw, cols, outs, rows, n).tile == 0;
+    const double share = !big ? 0.3 : dt == FSDPPACK_E4M3 ? 0.09 : 0.25;
+    return product_us * share > 4.0 + elements * 0.5e-6;
+}
+
 namespace {
 
 // Rows that 16-byte chunks can be taken from whole: `width` elements of a row
@@ -782,6 +800,9 @@ int launch_tile(GemmArgs &g, void *stream, void *e0, void *e1)
     constexpr int step_i = KIND == kGemmGated ? TI / 2 : TI;
     g.tiles_i = static_cast<int32_t>((g.I + step_i - 1) / step_i);
     g.tiles_j = static_cast<int32_t>((g.J + TJ - 1) / TJ);
+    const int64_t steps = (g.R + BK - 1) / BK * g.segs;
+    g.split_steps = steps / g.splits;
+    g.longer = static_cast<int32_t>(steps % g.splits);
     const int64_t tiles = int64_t{g.tiles_i} * g.tiles_j * g.splits * g.outs;
     const dim3 grid(static_cast<uint32_t>((tiles + kXcds - 1) / kXcds * kXcds)), block(64 * WI * WJ);
     LAUNCH((gemm_kernel<KIND, ADT, DMA_A, DMA_B, TI, TJ, WI, WJ>), grid, block, g);

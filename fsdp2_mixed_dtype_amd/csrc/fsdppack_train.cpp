@@ -160,17 +160,39 @@ int64_t partial_bytes(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
     return splits > 1 ? int64_t{4} * splits * outs * I * J : 0;
 }
 
+// Room for an 8-bit x's values in bf16 where the product reads those; dt < 0:
+// for either format.
+int64_t converted_ld(int64_t cols) { return round_up(cols, 8); }
+int64_t converted_bytes(int64_t rows, int64_t cols, int64_t outs, int n, int32_t dt)
+{
+    const bool any = dt < 0 ? gemm_reads_converted(rows, cols, outs, n, FSDPPACK_E4M3) ||
+                                  gemm_reads_converted(rows, cols, outs, n, FSDPPACK_INT8)
+                            : gemm_reads_converted(rows, cols, outs, n, dt);
+    return any ? round_up(rows * converted_ld(cols) * 2, 256) : 0;
+}
+
+// Write x's values to `space` and let `x` name them; counts the launch.
+int convert(Mat &x, int64_t rows, int64_t cols, void *space, void *stream, void *e0, int *launches)
+{
+    const Mat values{space, nullptr, converted_ld(cols), FSDPPACK_BF16};
+    const int e = launch_checkpoint(values, x, rows, cols, false, stream, e0, nullptr);
+    x = values;
+    ++*launches;
+    return e;
+}
+
 struct GatedSpace {
-    int64_t ld, half, partial, bytes;
+    int64_t ld, half, converted, partial, bytes;
 };
 
-GatedSpace gated_space(int64_t rows, int64_t ffn, int64_t cols)
+GatedSpace gated_space(int64_t rows, int64_t ffn, int64_t cols, int32_t x_dt)
 {
     GatedSpace s;
     s.ld = round_up(ffn, 8);
     s.half = round_up(rows * s.ld * 2, 256);
+    s.converted = converted_bytes(rows, cols, ffn, 2, x_dt);
     s.partial = std::max(partial_bytes(kGemmDx, cols, rows, ffn, 1), partial_bytes(kGemmDw, cols, ffn, rows, 2));
-    s.bytes = 2 * s.half + s.partial;
+    s.bytes = 2 * s.half + s.converted + s.partial;
     return s;
 }
 
@@ -332,7 +354,7 @@ int fsdppack_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t i
 try {
     Check c{"weight_grad_workspace"};
     if (!sizes_ok(c, rows, out_features, in_features, bytes)) return c.rc;
-    *bytes = partial_bytes(kGemmDw, in_features, out_features, rows, 1);
+    *bytes = converted_bytes(rows, in_features, out_features, 1, -1) + partial_bytes(kGemmDw, in_features, out_features, rows, 1);
     return FSDPPACK_OK;
 } catch (const std::bad_alloc &) {
     return FSDPPACK_ENOMEM;
@@ -348,9 +370,10 @@ try {
     if (!c.shape(x, "x") || !c.shape(dout, "dout")) return c.rc;
     const int64_t rows = x->rows, cols = x->cols, outs = dout->cols;
     if (!c.matrix(x, "x", rows, cols, kBf16 | kEight, &g.a[0]) || !c.matrix(dout, "dout", rows, outs, kBf16, &g.b[0]) ||
-        !c.matrix(dweight, "dweight", outs, cols, kDense, &g.out[0]) || !product_ok(c, cols, outs, 1))
+        !c.matrix(dweight, "dweight", outs, cols, kDense, &g.out[0]) || !product_ok(c, cols, outs, 1) ||
+        !elements_ok(c, rows, cols))
         return c.rc;
-    const int64_t need = partial_bytes(kGemmDw, cols, outs, rows, 1);
+    const int64_t room = converted_bytes(rows, cols, outs, 1, x->dtype), need = room + partial_bytes(kGemmDw, cols, outs, rows, 1);
     if (!workspace_ok(c, workspace, workspace_bytes, need)) return c.rc;
     Spans s;
     s.put(g.a[0], rows, cols, false, "x");
@@ -358,16 +381,20 @@ try {
     s.put(g.out[0], outs, cols, true, "dweight");
     s.put(workspace, 1, need, 0, true, "workspace");
     if (s.overlap(c)) return c.rc;
-    g.partial = static_cast<float *>(workspace);
+    int total = 0, launches = 0;
+    if (room > 0) {
+        if (int rc = convert(g.a[0], rows, cols, workspace, stream, e0, &total)) return report_hip(rc, c.call);
+        e0 = nullptr;
+    }
+    g.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + room);
     g.I = cols;
     g.J = outs;
     g.R = rows;
     g.segs = 1;
     g.outs = 1;
     g.splits = gemm_splits(kGemmDw, cols, outs, rows, 1);
-    int launches = 0;
     const int e = launch_gemm(kGemmDw, g, stream, e0, e1, &launches);
-    return finish(e, launches, c.call);
+    return finish(e, total + launches, c.call);
 } catch (const std::bad_alloc &) {
     return FSDPPACK_ENOMEM;
 }
@@ -414,7 +441,7 @@ int fsdppack_gated_backward_workspace(int64_t rows, int64_t ffn, int64_t cols, i
 try {
     Check c{"gated_backward_workspace"};
     if (!sizes_ok(c, rows, ffn, cols, bytes)) return c.rc;
-    *bytes = gated_space(rows, ffn, cols).bytes;
+    *bytes = gated_space(rows, ffn, cols, -1).bytes;
     return FSDPPACK_OK;
 } catch (const std::bad_alloc &) {
     return FSDPPACK_ENOMEM;
@@ -439,9 +466,9 @@ try {
         !c.matrix(dx, "dx", rows, cols, kDense, &gx.out[0]) || !c.matrix(dw_gate, "dw_gate", ffn, cols, kDense, &gw.out[0]) ||
         !c.matrix(dw_up, "dw_up", ffn, cols, kDense, &gw.out[1]) ||
         (out != nullptr && !c.matrix(out, "out", rows, ffn, kBf16, &e.out)) || !product_ok(c, cols, ffn, 2) ||
-        !product_ok(c, cols, rows, 1) || !elements_ok(c, rows, ffn))
+        !product_ok(c, cols, rows, 1) || !elements_ok(c, rows, ffn) || !elements_ok(c, rows, cols))
         return c.rc;
-    const GatedSpace sp = gated_space(rows, ffn, cols);
+    const GatedSpace sp = gated_space(rows, ffn, cols, x->dtype);
     if (!workspace_ok(c, workspace, workspace_bytes, sp.bytes)) return c.rc;
     Spans s;
     s.put(e.dout, rows, ffn, false, "dout");
@@ -470,7 +497,7 @@ try {
         ++total;
         gx.b[0] = Mat{e.dgate, nullptr, sp.ld, FSDPPACK_BF16};
         gx.b[1] = Mat{e.dup, nullptr, sp.ld, FSDPPACK_BF16};
-        gx.partial = reinterpret_cast<float *>(ws + 2 * sp.half);
+        gx.partial = reinterpret_cast<float *>(ws + 2 * sp.half + sp.converted);
         gx.I = cols;
         gx.J = rows;
         gx.R = ffn;
@@ -480,9 +507,11 @@ try {
         if (int rc = launch_gemm(kGemmDx, gx, stream, nullptr, nullptr, &n)) return report_hip(rc, c.call);
         total += n;
     }
+    if (sp.converted > 0)
+        if (int rc = convert(gw.a[0], rows, cols, ws + 2 * sp.half, stream, nullptr, &total)) return report_hip(rc, c.call);
     gw.b[0] = Mat{e.dgate, nullptr, sp.ld, FSDPPACK_BF16};
     gw.b[1] = Mat{e.dup, nullptr, sp.ld, FSDPPACK_BF16};
-    gw.partial = reinterpret_cast<float *>(ws + 2 * sp.half);
+    gw.partial = reinterpret_cast<float *>(ws + 2 * sp.half + sp.converted);
     gw.I = cols;
     gw.J = ffn;
     gw.R = rows;

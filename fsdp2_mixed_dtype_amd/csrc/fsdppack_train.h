@@ -65,6 +65,8 @@ struct GemmArgs {
     int64_t I, J, R;
     int32_t segs, outs, splits, act;
     int32_t tiles_i, tiles_j;
+    int64_t split_steps;              // steps of a split, the first `longer` of them one more
+    int32_t longer;
 };
 
 enum GemmKind { kGemmGated, kGemmDx, kGemmDw };
@@ -76,6 +78,8 @@ int launch_norm_backward(const NormBackArgs &a, void *stream, void *e0, void *e1
 int launch_gate_backward(const GateArgs &a, void *stream, void *e0, void *e1);
 // Splits of the reduction a product uses, and its partial sums' bytes.
 int gemm_splits(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs);
+// Whether a weight gradient reads an 8-bit x as bf16 values written first.
+bool gemm_reads_converted(int64_t rows, int64_t cols, int64_t outs, int n, int32_t dt);
 int launch_gemm(GemmKind kind, GemmArgs a, void *stream, void *e0, void *e1, int *launches);
 
 }  // namespace fsdppack

@@ -391,8 +391,9 @@ int fsdppack_norm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes)
 /* A linear layer's weight gradient, dweight[o, i] = sum over rows r of
  * dout[r, o] * x[r, i] (zero when rows = 0).  dout: bf16 [rows, outs].  x:
  * [rows, cols], bf16 or an 8-bit checkpoint, whose values enter the product
- * exactly.  dweight: dense [outs, cols], in the dtype its gradient is packed
- * in.  At most two launches.  Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+ * exactly (with many outputs they are written to the workspace in bf16
+ * first).  dweight: dense [outs, cols], in the dtype its gradient is packed
+ * in.  At most three launches.  Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
 int fsdppack_weight_grad(const fsdppack_matrix *dout, const fsdppack_matrix *x, const fsdppack_matrix *dweight,
                          void *workspace, int64_t workspace_bytes, void *stream);
 int fsdppack_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features, int64_t *bytes);
@@ -418,8 +419,8 @@ int fsdppack_gated_forward(int32_t act, const fsdppack_matrix *x, const fsdppack
  * the dtype their gradients are packed in (zero when rows = 0).  out: NULL,
  * or a bf16 [rows, ffn] matrix that receives act(g) * u again, for the
  * weight gradient of the projection behind the block.  workspace:
- * gated_backward_workspace bytes (dg, du and partial sums).  At most five
- * launches.  Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
+ * gated_backward_workspace bytes (dg, du, x's values where they are read as
+ * bf16, and partial sums).  At most six launches.  Errors: EINVAL, EDTYPE, EHIP, ENOMEM. */
 int fsdppack_gated_backward(int32_t act, const fsdppack_matrix *dout, const fsdppack_matrix *x,
                             const fsdppack_matrix *w_gate, const fsdppack_matrix *w_up, const fsdppack_matrix *gate,
                             const fsdppack_matrix *up, const fsdppack_matrix *dx, const fsdppack_matrix *dw_gate,

@@ -360,6 +360,28 @@ def test_weight_grad_random(rows, outs, cols, x_kind):
     assert bool(torch.isnan(dw.as_strided((outs - 1, 4), (cols + 4, 1), cols)).all())
 
 
+@pytest.mark.parametrize("fmt", EIGHT)
+@pytest.mark.parametrize("rows,outs,cols", [(300, 64, 128), (2048, 6000, 1000), (8192, 4096, 512), (1025, 8200, 2047)])
+def test_weight_grad_of_a_checkpoint_is_that_of_its_values(fmt, rows, outs, cols):
+    """Small and large products, on both sides of where the values are written
+    out first: the same bits as from a bf16 x holding them."""
+    g = gen(rows)
+    q = save(randn(g, rows, cols), fmt)
+    dy, x = randn(g, rows, outs), fp.checkpoint_load(q, torch.empty(rows, cols, dtype=BF, device="cuda"))
+    ws = workspace(fp.weight_grad_workspace(rows, outs, cols))
+    got, want = torch.empty(outs, cols, device="cuda"), torch.empty(outs, cols, device="cuda")
+    fp.weight_grad(dy, q, got, ws)
+    fp.weight_grad(dy, x, want, ws)
+    assert torch.equal(got, want)
+    gate, wg = randn(g, rows, outs), randn(g, outs, cols, std=0.05)
+    ws = workspace(fp.gated_backward_workspace(rows, outs, cols))
+    res = [[torch.empty(rows, cols, device="cuda"), torch.empty(outs, cols, device="cuda"), torch.empty(outs, cols, device="cuda")]
+           for _ in range(2)]
+    for r, arg in zip(res, (q, x)):
+        fp.gated_backward(dy, arg, wg, wg, gate, gate, *r, ws)
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
 def test_weight_grad_non_finite():
     """A NaN or infinity of x reaches its own column of dW only, also from 8 bits."""
     for fmt in (None,) + EIGHT:
