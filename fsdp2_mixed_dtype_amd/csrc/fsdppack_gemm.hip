@@ -245,60 +245,41 @@ __device__ __forceinline__ bf16x8 fragment(const uint16_t *tile, int at, int s)
     }
 }
 
-// Two packed quads per lane (columns 8 q + 4 h + 0..3 of q = 0 and 1, h =
-// lane / 32) -> eight consecutive columns per lane: those of q = h.
-__device__ __forceinline__ u32x4 join_halves(u32x2 q0, u32x2 q1)
+// Results on their way to memory.  The matrix cores leave 32 rows j = lane % 32
+// with quads of four columns (8 q + 4 (lane / 32) + 0..3, q < 4) of each piece;
+// stored like that, an instruction would touch 32 rows with 16 bytes each.  A
+// wavefront lays 32 rows of up to 128 bytes out in its own part of LDS instead
+// (the operands' images are free by then) and writes whole lines: 16-byte
+// pieces, 8 lanes a row.  Whole lines can go past L2 (non-temporal), which the
+// operands then have to themselves: gated forward 8192 x 4096 x 12288 without
+// kept projections 1260 us from the cores' layout, 1269 staged, 1190 staged
+// and non-temporal; with e4m3 projections 1328, 1318, 1254.
+constexpr int kStagePitch = 144;      // bytes; 16 more than a row's, which spreads the rows over the banks
+
+__device__ __forceinline__ void stage_bf16(char *stage, int byte, const float *v)
 {
-    const auto x = __builtin_amdgcn_permlane32_swap(q0.x, q1.x, false, false);
-    const auto y = __builtin_amdgcn_permlane32_swap(q0.y, q1.y, false, false);
-    return u32x4{x[0], y[0], x[1], y[1]};
+    const int lane = threadIdx.x & 63;
+    char *at = stage + (lane & 31) * kStagePitch + byte + (lane >> 5) * 8;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<u32x2 *>(at + 16 * q) = u32x2{pack_bf16(v[4 * q], v[4 * q + 1]), pack_bf16(v[4 * q + 2], v[4 * q + 3])};
 }
 
-// A piece's row (32 columns from `col` of the tile's row, 16 per lane as the
-// matrix cores leave them) as bf16; `cols` of the tile's columns exist.  Both
-// halves of the wavefront call it.
-__device__ __forceinline__ void store_row(uint16_t *row, int col, int cols, bool row_ok, const float *v)
+__device__ __forceinline__ void stage_fp32(char *stage, const float *v)
 {
-    const int h = (threadIdx.x >> 5) & 1;
+    const int lane = threadIdx.x & 63;
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    char *at = stage + (lane & 31) * kStagePitch + (lane >> 5) * 16;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const float *q = v + 8 * p;
-        const u32x4 w = join_halves(u32x2{pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3])},
-                                    u32x2{pack_bf16(q[4], q[5]), pack_bf16(q[6], q[7])});
-        const int c = col + 16 * p + 8 * h;
-        if (!row_ok || c >= cols) continue;
-        if (c + 8 <= cols) {
-            *reinterpret_cast<u32x4u *>(row + c) = u32x4u{w.x, w.y, w.z, w.w};
-        } else {
-#pragma unroll 1
-            for (int i = 0; c + i < cols; ++i) row[c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-        }
-    }
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<f32x4 *>(at + 32 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
 }
 
-__device__ __forceinline__ void store_row_fp32(float *row, int col, int cols, bool row_ok, const float *v)
-{
-    const int h = (threadIdx.x >> 5) & 1;
-    if (!row_ok) return;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int c = col + 8 * q + 4 * h;
-        if (c + 4 <= cols) {
-            *reinterpret_cast<f32x4u *>(row + c) = f32x4u{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (c + i < cols) row[c + i] = v[4 * q + i];
-        }
-    }
-}
-
-// A projection's piece kept for the backward pass.  In 8 bits, lanes l and
-// l + 32 hold one scale group (32 columns of a row) between them.
+// A piece in 8 bits; lanes l and l + 32 hold one scale group (32 columns of a
+// row) between them.  Returns the group's scale byte.
 template <int DT>
-__device__ __forceinline__ void keep_row8(uint8_t *row, uint8_t *scales, int col, int cols, bool row_ok, const float *v)
+__device__ __forceinline__ uint32_t stage_codes(char *stage, int byte, const float *v)
 {
-    const int h = (threadIdx.x >> 5) & 1;
+    const int lane = threadIdx.x & 63;
     uint32_t bits = max(top_bits8(v), top_bits8(v + 8));
     bits = max(bits, static_cast<uint32_t>(__shfl_xor(static_cast<int>(bits), 32)));
     uint32_t w[4];
@@ -314,30 +295,63 @@ __device__ __forceinline__ void keep_row8(uint8_t *row, uint8_t *scales, int col
         encode8<DT, false>(v, e, w[0], w[1]);
         encode8<DT, false>(v + 8, e, w[2], w[3]);
     }
-    // dword q: columns 8 q + 4 h; lanes below 32 get columns 0..15, the others 16..31
-    const u32x4 b = join_halves(u32x2{w[0], w[1]}, u32x2{w[2], w[3]});
-    const int c = col + 16 * h;
-    if (!row_ok || c >= cols) return;
-    // b = own q0, q1 of the lower lane, then of the upper: columns 0-3, 8-11, 4-7, 12-15
-    const uint32_t d[4] = {b.x, b.z, b.y, b.w};
-    if (c + 16 <= cols) {
-        typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
-        *reinterpret_cast<u32x4b *>(row + c) = u32x4b{d[0], d[1], d[2], d[3]};
-    } else {
+    char *at = stage + (lane & 31) * kStagePitch + byte + (lane >> 5) * 4;
 #pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (c + i < cols) row[c + i] = static_cast<uint8_t>(d[i >> 2] >> (8 * (i & 3)));
-    }
-    if (h == 0) scales[col / kGroup] = static_cast<uint8_t>(e + 127);
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t *>(at + 8 * q) = w[q];
+    return static_cast<uint32_t>(e + 127);
 }
 
-__device__ __forceinline__ void keep_row(const Mat &o, int64_t j, int64_t i0, int64_t I, int col, int cols, bool row_ok, const float *v)
+// Write BYTES of each staged row to memory: row r at out + r * pitch, if r <
+// rows; of its bytes the first `bytes` (elements of SIZE) exist.
+template <int BYTES, int SIZE>
+__device__ __forceinline__ void flush(const char *stage, char *out, int64_t pitch, int rows, int bytes)
 {
-    if (o.p == nullptr) return;
-    if (o.dt == FSDPPACK_BF16) return store_row(static_cast<uint16_t *>(o.p) + j * o.ld + i0, col, cols, row_ok, v);
-    uint8_t *row = static_cast<uint8_t *>(o.p) + j * o.ld + i0, *scales = o.scales + j * ((I + kGroup - 1) / kGroup) + i0 / kGroup;
-    if (o.dt == FSDPPACK_E4M3) keep_row8<FSDPPACK_E4M3>(row, scales, col, cols, row_ok, v);
-    else keep_row8<FSDPPACK_INT8>(row, scales, col, cols, row_ok, v);
+    constexpr int PER = BYTES / 16, EACH = 64 / PER;      // lanes a row, rows an instruction
+    const int lane = threadIdx.x & 63, byte = lane % PER * 16;
+    typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
+    typedef std::conditional_t<SIZE == 1, u32x4b, u32x4u> Wide;
+#pragma unroll
+    for (int i = 0; i < 32 / EACH; ++i) {
+        const int r = i * EACH + lane / PER;
+        const char *from = stage + r * kStagePitch + byte;
+        char *to = out + r * pitch + byte;
+        if (r >= rows) continue;
+        if (byte + 16 <= bytes) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(from);
+            __builtin_nontemporal_store(Wide{w.x, w.y, w.z, w.w}, reinterpret_cast<Wide *>(to));
+        } else {
+#pragma unroll 1
+            for (int e = 0; byte + e < bytes; e += SIZE) {
+                if constexpr (SIZE == 1) to[e] = from[e];
+                else if constexpr (SIZE == 2) *reinterpret_cast<uint16_t *>(to + e) = *reinterpret_cast<const uint16_t *>(from + e);
+                else *reinterpret_cast<uint32_t *>(to + e) = *reinterpret_cast<const uint32_t *>(from + e);
+            }
+        }
+    }
+}
+
+// 32 rows of PIECES pieces (v[p]: this lane's 16 values) in bf16 or 8 bits, to
+// rows j.. and columns i.. of o; `rows` and `cols` of them exist.
+template <int PIECES>
+__device__ __forceinline__ void keep_rows(const Mat &o, char *stage, int64_t j, int64_t i, int64_t I, int rows, int cols, const float (*v)[16])
+{
+    if (o.dt == FSDPPACK_BF16) {
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) stage_bf16(stage, 64 * p, v[p]);
+        flush<64 * PIECES, 2>(stage, static_cast<char *>(o.p) + (j * o.ld + i) * 2, o.ld * 2, rows, cols * 2);
+        return;
+    }
+    uint32_t scales = 0;
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+        scales |= (o.dt == FSDPPACK_E4M3 ? stage_codes<FSDPPACK_E4M3>(stage, 32 * p, v[p]) : stage_codes<FSDPPACK_INT8>(stage, 32 * p, v[p])) << (8 * p);
+    flush<32 * PIECES, 1>(stage, static_cast<char *>(o.p) + j * o.ld + i, o.ld, rows, cols);
+    const int lane = threadIdx.x & 63;
+    uint8_t *at = o.scales + (j + lane) * ((I + kGroup - 1) / kGroup) + i / kGroup;
+    if (lane >= rows || lane >= 32) return;
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+        if (32 * p < cols) at[p] = static_cast<uint8_t>(scales >> (8 * p));
 }
 
 // One TI x TJ output tile per block of WI x WJ wavefronts.
@@ -355,7 +369,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
     constexpr bool ATR = KIND != kGemmGated, BTR = KIND == kGemmDw;
     constexpr int THREADS = 64 * WI * WJ, NA = TI / WI / 32, NB = TJ / WJ / 32;
     __shared__ __align__(1024) uint16_t sa0[TI * BK], sb0[TJ * BK], sa1[TI * BK], sb1[TJ * BK];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     // each die takes a contiguous run of tiles, in bands of 4 tile rows of
     // the output, so that its neighbours' operands meet in its L2
@@ -508,38 +522,67 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
         }
     }
 
-    // lane: output row j = lane % 32, output columns 8 q + 4 (lane / 32) + 0..3 for q < 4
-    const int cols = static_cast<int>(i_end - i0 < TI ? i_end - i0 : TI);
+    // a wavefront's part of LDS, 32 rows of 144 bytes: half of the wavefronts in
+    // each of A's images, which nobody reads any more
+    constexpr int HALF = WI * WJ / 2;
+    static_assert(HALF * 32 * kStagePitch <= TI * BK * 2, "the staged rows fit an image");
+    char *stage = reinterpret_cast<char *>(wave < HALF ? sa0 : sa1) + wave % HALF * 32 * kStagePitch;
+    const int cols = static_cast<int>(i_end - i0 < TI ? i_end - i0 : TI);     // of the tile's, those that exist
+    constexpr int PIECES = NA >= 2 && KIND != kGemmGated ? 2 : KIND == kGemmGated && NA >= 4 ? 2 : 1;    // 64 columns at a time, or 32
 #pragma unroll
     for (int m = 0; m < NB; ++m) {
-        const int64_t j = j0 + piece_b(m) + (lane & 31);
-        const bool row_ok = j < g.J;
+        const int64_t j = j0 + piece_b(m);
+        const int rows = static_cast<int>(g.J - j < 32 ? g.J - j : 32);      // may be negative
         if constexpr (KIND == kGemmGated) {
-            uint16_t *row = static_cast<uint16_t *>(g.out[0].p) + j * g.out[0].ld + i0;
 #pragma unroll
-            for (int p = 0; p < NA / 2; ++p) {
-                float gv[16], uv[16], hv[16];
+            for (int p = 0; p < NA / 2; p += PIECES) {
+                float gv[PIECES][16], uv[PIECES][16];
+                const int at = piece_a(p);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    gv[e] = acc[p][m][e];
-                    uv[e] = acc[p + NA / 2][m][e];
-                    hv[e] = activation_alone(g.act, gv[e]) * uv[e];
+                for (int d = 0; d < PIECES; ++d) {
+                    float hv[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        gv[d][e] = acc[p + d][m][e];
+                        uv[d][e] = acc[p + d + NA / 2][m][e];
+                        hv[e] = activation_alone(g.act, gv[d][e]) * uv[d][e];
+                    }
+                    stage_bf16(stage, 64 * d, hv);
                 }
-                store_row(row, piece_a(p), cols, row_ok, hv);
-                keep_row(g.gate, j, i0, g.I, piece_a(p), cols, row_ok, gv);
-                keep_row(g.up, j, i0, g.I, piece_a(p), cols, row_ok, uv);
+                flush<64 * PIECES, 2>(stage, static_cast<char *>(g.out[0].p) + (j * g.out[0].ld + i0 + at) * 2, g.out[0].ld * 2, rows,
+                                      (cols - at) * 2);
+                if (g.gate.p) keep_rows<PIECES>(g.gate, stage, j, i0 + at, g.I, rows, cols - at, gv);
+                if (g.up.p) keep_rows<PIECES>(g.up, stage, j, i0 + at, g.I, rows, cols - at, uv);
             }
         } else {
             const Mat &o = g.out[z];
-            float *part = g.partial + ((int64_t{z} * g.splits + split) * g.J + j) * g.I + i0;
+            const bool wide = g.splits > 1 || o.dt == FSDPPACK_FP32;
+            // fp32: the output, or this split's partial sums
+            char *to = g.splits > 1 ? reinterpret_cast<char *>(g.partial + ((int64_t{z} * g.splits + split) * g.J + j) * g.I + i0)
+                                    : static_cast<char *>(o.p) + (j * o.ld + i0) * (wide ? 4 : 2);
+            const int64_t pitch = g.splits > 1 ? g.I * 4 : o.ld * (wide ? 4 : 2);
 #pragma unroll
-            for (int p = 0; p < NA; ++p) {
-                float v[16];
+            for (int p = 0; p < NA; p += PIECES) {
+                const int at = piece_a(p);
+                if (wide) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = acc[p][m][e];
-                if (g.splits > 1) store_row_fp32(part, piece_a(p), cols, row_ok, v);
-                else if (o.dt == FSDPPACK_BF16) store_row(static_cast<uint16_t *>(o.p) + j * o.ld + i0, piece_a(p), cols, row_ok, v);
-                else store_row_fp32(static_cast<float *>(o.p) + j * o.ld + i0, piece_a(p), cols, row_ok, v);
+                    for (int d = 0; d < PIECES; ++d) {
+                        float v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = acc[p + d][m][e];
+                        stage_fp32(stage, v);
+                        flush<128, 4>(stage, to + (at + 32 * d) * 4, pitch, rows, (cols - at - 32 * d) * 4);
+                    }
+                } else {
+#pragma unroll
+                    for (int d = 0; d < PIECES; ++d) {
+                        float v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = acc[p + d][m][e];
+                        stage_bf16(stage, 64 * d, v);
+                    }
+                    flush<64 * PIECES, 2>(stage, to + at * 2, pitch, rows, (cols - at) * 2);
+                }
             }
         }
     }
