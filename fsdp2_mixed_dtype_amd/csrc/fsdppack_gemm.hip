@@ -97,7 +97,7 @@ struct Loader {
     // Where the next step's tile starts, and each unit's offset from there in bytes.
     const char *at, *at2, *next;      // next: the second segment's first step
     const uint8_t *scale_at;
-    int64_t pitch, scale_pitch;
+    int64_t pitch, scale_pitch, line; // line: elements between rows
     uint32_t off[kUnits], scale_off[DT == FSDPPACK_BF16 ? 1 : kUnits];
 
     // Set out at reduction element r0 of the tile whose first row (column,
@@ -110,21 +110,29 @@ struct Loader {
         at = static_cast<const char *>(m.p) + first;
         if constexpr (TWO) at2 = static_cast<const char *>(m2.p) + (t0 * m2.ld + r0) * SIZE;
         pitch = (TR ? BK * m.ld : BK) * SIZE;
+        line = m.ld;
         const int32_t nt = static_cast<int32_t>(W - t0 < T ? W - t0 : T);
 #pragma unroll
         for (int c = 0; c < kUnits; ++c) {
             const int32_t ld = static_cast<int32_t>(TWO && c * kRows >= T / 2 ? m2.ld : m.ld);
             const int row = row0 + c * kRows, col = DMA ? swizzled<TR, T>(row, col0 >> 3) << 3 : col0;
             const int r = TWO ? row & (T / 2 - 1) : row;
-            off[c] = !DMA || (TR ? col : r) < nt ? static_cast<uint32_t>(r * ld + col) * SIZE : kOutside;
+            if constexpr (DMA) {
+                off[c] = (TR ? col : r) < nt ? static_cast<uint32_t>(r * ld + col) * SIZE : kOutside;
+            } else {
+                // rows (columns, TR) that are not there are read from ones that
+                // are: they only make results that are not stored
+                const int rr = TR || r < nt ? r : nt - 1, cc = !TR || col < nt ? col : 0;
+                off[c] = static_cast<uint32_t>(rr * ld + cc) * SIZE;
+            }
         }
         if constexpr (DT != FSDPPACK_BF16) {
             static_assert(TR, "8-bit operands have their scale groups across the tile");
-            const int32_t groups = static_cast<int32_t>((W + kGroup - 1) / kGroup);
+            const int32_t groups = static_cast<int32_t>((W + kGroup - 1) / kGroup), nt0 = static_cast<int32_t>(W - t0 < T ? W - t0 : T);
             scale_at = m.scales + r0 * groups + t0 / kGroup;
             scale_pitch = int64_t{BK} * groups;
 #pragma unroll
-            for (int c = 0; c < kUnits; ++c) scale_off[c] = (row0 + c * kRows) * groups + col0 / kGroup;
+            for (int c = 0; c < kUnits; ++c) scale_off[c] = (row0 + c * kRows) * groups + (col0 < nt0 ? col0 / kGroup : 0);
         }
     }
 
@@ -161,7 +169,9 @@ struct Loader {
     }
 
     // The same through registers.  `rest`: rows (columns, TR) of the tile
-    // that exist; WHOLE: all of them, and BK reduction elements.
+    // that exist; WHOLE: BK reduction elements, and a wide load from any unit
+    // stays inside the matrix (TR: it may run past its row's end into the
+    // next row, whose values make results that are not stored).
     template <bool WHOLE>
     __device__ __forceinline__ void start_reg(int64_t left, int64_t rest)
     {
@@ -179,7 +189,9 @@ struct Loader {
             }
             reg[c] = u32x4{0, 0, 0, 0};
             if constexpr (DT != FSDPPACK_BF16) scale[c] = 0;
-            if (WHOLE || n == kUnit) {
+            // TR: whether a wide load that runs past the row's end is still in the matrix
+            const bool within = TR && n > 0 && (left - 1 - (threadIdx.x * kUnit / kPerRow + c * kRows)) * line + n >= kUnit;
+            if (WHOLE || n == kUnit || within) {
                 const Wide w = *reinterpret_cast<const Wide *>(p);
                 reg[c] = u32x4{w.x, w.y, w.z, w.w};
             } else {
@@ -396,10 +408,14 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
     Loader<BTR, TJ, THREADS, FSDPPACK_BF16, DMA_B, false> lb;
     // Steps that are whole and need nothing but the last one's addresses
     // carried on (or switched to the other segment's, where the two have the
-    // same strides); through registers, only in tiles of which all exists.
-    const bool inside = (DMA_A || i_end - i0 >= (KIND == kGemmGated ? TI / 2 : TI)) && (DMA_B || g.J - j0 >= TJ);
-    const bool alike = KIND != kGemmDx || (g.R % BK == 0 && g.a[0].ld == g.a[1].ld && g.b[0].ld == g.b[1].ld);
-    const int64_t plain_end = inside && alike ? g.R / BK * g.segs - s0 : 0;
+    // same strides).  A strided operand that comes through registers in a tile
+    // that is not all there reads past its rows' ends: not in the last step,
+    // whose last row ends the matrix, nor where a row is shorter than a load.
+    const int64_t first_ld = g.b[KIND == kGemmDw ? z : 0].ld;
+    const bool over = (ATR && !DMA_A && i_end - i0 < TI) || (BTR && !DMA_B && g.J - j0 < TJ);
+    const bool alike = KIND != kGemmDx || (!over && g.R % BK == 0 && g.a[0].ld == g.a[1].ld && g.b[0].ld == g.b[1].ld);
+    const bool wide_rows = !over || ((!ATR || g.a[0].ld >= 16) && (!BTR || first_ld >= 16));
+    const int64_t plain_end = alike && wide_rows ? (g.R - over) / BK * g.segs - s0 : 0;
     const Mat &first_b = g.b[KIND == kGemmDw ? z : 0];
     // Start bringing in A's half of step k, then (later) B's.  WHOLE: k > 0 is
     // a plain step.
@@ -511,14 +527,29 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
         meet();
         if (n > 1) start_a(any, 1, sa1);
         read(0, sa0, sb0, 0);
-        int64_t k = 0;
-        for (int64_t pairs = ((plain_end < n ? plain_end : n) - 2) / 2; pairs > 0; --pairs, k += 2) {
-            do_step(plain, k, sa0, sb0, sa1, sb1);
-            do_step(plain, k + 1, sa1, sb1, sa0, sb0);
-        }
-        for (; k < n; k += 2) {
-            do_step(any, k, sa0, sb0, sa1, sb1);
-            if (k + 1 < n) do_step(any, k + 1, sa1, sb1, sa0, sb0);
+        if constexpr (KIND == kGemmDx && !DMA_A) {
+            // plain pairs of each segment, then its last steps and the next one's first
+            for (int64_t k = 0; k < n;) {
+                const int64_t next = s0 + k + 1;
+                const int seg = next >= steps1;
+                const int64_t end = seg * steps1 + (g.R - over) / BK - s0;
+                for (int64_t pairs = next > seg * steps1 && wide_rows ? ((end < n ? end : n) - (k + 2)) / 2 : 0; pairs > 0; --pairs, k += 2) {
+                    do_step(plain, k, sa0, sb0, sa1, sb1);
+                    do_step(plain, k + 1, sa1, sb1, sa0, sb0);
+                }
+                do_step(any, k, sa0, sb0, sa1, sb1);
+                if (++k < n) do_step(any, k, sa1, sb1, sa0, sb0), ++k;
+            }
+        } else {
+            int64_t k = 0;
+            for (int64_t pairs = ((plain_end < n ? plain_end : n) - 2) / 2; pairs > 0; --pairs, k += 2) {
+                do_step(plain, k, sa0, sb0, sa1, sb1);
+                do_step(plain, k + 1, sa1, sb1, sa0, sb0);
+            }
+            for (; k < n; k += 2) {
+                do_step(any, k, sa0, sb0, sa1, sb1);
+                if (k + 1 < n) do_step(any, k + 1, sa1, sb1, sa0, sb0);
+            }
         }
     }
 
@@ -545,6 +576,14 @@ __global__ void __launch_bounds__(64 * WI * WJ, TI == 256 || TJ == 128 ? 2 : 3) 
                     for (int e = 0; e < 16; ++e) {
                         gv[d][e] = acc[p + d][m][e];
                         uv[d][e] = acc[p + d + NA / 2][m][e];
+                    }
+                    // columns that are not there do not count for their scale group
+                    if (!DMA_A && cols - at < 32 * (d + 1))
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (32 * d + 8 * (e >> 2) + 4 * static_cast<int>(threadIdx.x >> 5 & 1) + (e & 3) >= cols - at) gv[d][e] = uv[d][e] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
                         hv[e] = activation_alone(g.act, gv[d][e]) * uv[d][e];
                     }
                     stage_bf16(stage, 64 * d, hv);

@@ -45,7 +45,7 @@
  *    outside the bucket being packed).
  *  - `stream` is a hipStream_t (NULL = the default stream).  Every compute
  *    call enqueues one kernel launch on it (none when there is nothing to
- *    write) and returns without waiting; argument errors are reported
+ *    write; some of the training operators several) and returns without waiting; argument errors are reported
  *    synchronously and enqueue nothing.
  *  - Every call returns FSDPPACK_OK (0) or a negative error code, and on
  *    error leaves a message for fsdppack_last_error() (per thread).  No

@@ -328,7 +328,7 @@ def integers(g, *shape, top=2):
 
 PRODUCTS = [(1, 1, 1), (1, 64, 64), (3, 5, 7), (64, 128, 128), (63, 127, 129), (65, 32, 96), (100, 130, 200), (128, 256, 256),
             (257, 300, 520), (1000, 96, 40), (2055, 512, 264), (4100, 70, 1000), (200, 1500, 1030), (0, 40, 72), (16384, 33, 65),
-            (300, 1024, 1024)]
+            (300, 1024, 1024), (1000, 300, 777), (2047, 511, 515), (640, 270, 13), (129, 9, 300)]
 
 
 @pytest.mark.parametrize("rows,outs,cols", PRODUCTS)
@@ -439,7 +439,7 @@ def act_reference(act, g):
 ACT = 200 * U
 
 GATED = [(1, 1, 1), (1, 64, 128), (1, 1024, 4096), (2, 40, 72), (17, 33, 65), (31, 512, 256), (33, 520, 300), (64, 64, 64), (100, 96, 40),
-         (129, 200, 520), (300, 1024, 192), (16, 4096, 100), (513, 264, 1030), (5, 1000, 2055)]
+         (129, 200, 520), (300, 1024, 192), (16, 4096, 100), (513, 264, 1030), (5, 1000, 2055), (300, 257, 333), (271, 130, 1001)]
 
 
 @pytest.mark.parametrize("act", [fp.SILU, fp.GELU_TANH])
