@@ -816,8 +816,8 @@ struct Cut {
 // per step, which grows from a CU with one block (and few busy CUs) to a full
 // card; split sums cost a second kernel and their writing and reading.  The
 // figures are microseconds measured on MI355X with each cut forced: 4096 x 512
-// x 2048 takes 76 us as 16 tiles of 256, 43 as 64 of 128, 26 as those in 4
-// splits; 8192 x 4096 x 4096 takes 259 as 256 of 256, 297 as 1024 of 128.
+// x 2048 takes 74 us as 16 tiles of 256, 40 as 64 of 128, 22 as those in 4
+// splits; 8192 x 4096 x 4096 takes 235 as 256 of 256, 265 as 1024 of 128.
 Cut cut_of(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
 {
     constexpr int kTi[3] = {256, 128, 128}, kTj[3] = {256, 128, 32}, kHeld[3] = {1, 2, 3};
@@ -852,18 +852,19 @@ Cut cut_of(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs)
 int gemm_splits(GemmKind kind, int64_t I, int64_t J, int64_t R, int outs) { return cut_of(kind, I, J, R, outs).splits; }
 
 // Codes converted on their way into LDS cost the product about 9 % (e4m3) or
-// 25 % (int8) of its time with 256 x 256 tiles and 30 % with 128 x 128, where
-// fewer matrix instructions cover them (8192 x 1024 x 4096: 115 us against
-// 86).  Converted once before, they cost a launch, their reading and twice
-// their writing (15 us for 8192 x 4096), whatever the number of outputs: worth
-// it from a few thousand outputs on.
+// 25 % (int8) of its time with 256 x 256 tiles, and 25 or 70 % with 128 x 128,
+// where fewer matrix instructions cover them (8192 x 1024 x 4096: 95 and 138 us
+// against 77 from bf16).  Converted once before, they cost a launch, their
+// reading and twice their writing whatever the number of outputs (there 85 and
+// 84 us in all): worth it from a few thousand outputs on.
 bool gemm_reads_converted(int64_t rows, int64_t cols, int64_t outs, int n, int32_t dt)
 {
     if (dt != FSDPPACK_E4M3 && dt != FSDPPACK_INT8) return false;
     const double elements = static_cast<double>(rows) * static_cast<double>(cols);
     const double product_us = 2.0 * elements * static_cast<double>(outs) * n / 1.3e9;
     const bool big = cut_of(kGemmDw, cols, outs, rows, n).tile == 0;
-    const double share = !big ? 0.3 : dt == FSDPPACK_E4M3 ? 0.09 : 0.25;
+    const bool e4m3 = dt == FSDPPACK_E4M3;
+    const double share = big ? (e4m3 ? 0.09 : 0.25) : (e4m3 ? 0.25 : 0.7);
     return product_us * share > 4.0 + elements * 0.5e-6;
 }
 

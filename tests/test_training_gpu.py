@@ -276,6 +276,23 @@ def test_norm_backward(kind, rows, cols, pad, x_kind, ddt, odt, gdt):
         assert torch.equal(again[0], dw) and torch.equal(again[1], dx)
 
 
+@pytest.mark.parametrize("cols", [96, 1000, 20000])
+def test_norm_backward_parts_not_wanted(cols):
+    """dbias alone, dweight alone, neither (no workspace): the same bits as both."""
+    g = gen(cols)
+    x, dy, w = randn(g, 37, cols), randn(g, 37, cols), randn(g, cols, dtype=F32)
+    stats, ws = torch.rand(37, 2, generator=g, device="cuda"), workspace(fp.norm_backward_workspace(37, cols))
+    new = lambda: torch.full((cols,), float("nan"), device="cuda")  # noqa: E731
+    dx, dw, db = torch.empty_like(x), new(), new()
+    fp.norm_backward(dy, x, w, stats, dx, dw, ws, dbias=db)
+    for want_w, want_b, space in ((None, new(), ws), (new(), None, ws), (None, None, None)):
+        other = torch.empty_like(x)
+        fp.norm_backward(dy, x, w, stats, other, want_w, space, dbias=want_b)
+        assert torch.equal(other, dx)
+        assert want_w is None or torch.equal(want_w, dw)
+        assert want_b is None or torch.equal(want_b, db)
+
+
 @pytest.mark.parametrize("kind", [fp.LAYER_NORM, fp.RMS_NORM])
 def test_norm_gradient_against_differences(kind):
     """dL of L = sum(out * dout) along a direction in x, w and b at once, by
@@ -708,6 +725,37 @@ def test_two_streams_at_once():
     for b, w in zip(got, want):
         for name in RESULTS:
             assert torch.equal(b[name], w[name]), name
+
+
+def test_four_host_threads():
+    """Calls from several host threads, each on its own stream and tensors."""
+    import threading
+    want, got = block(seed=8), [block(seed=8) for _ in range(4)]
+    for b in [want] + got:
+        b["dh"].fill_(0.01)
+    step(want)
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(b):
+        try:
+            torch.cuda.set_device(0)
+            s = torch.cuda.Stream()
+            for _ in range(10):
+                step(b, stream=s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(b,)) for b in got]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for b in got:
+        for name in RESULTS:
+            assert torch.equal(b[name], want[name]), name
 
 
 def test_captured_step_replays():
