@@ -679,15 +679,19 @@ int launch_norm_forward(const NormArgs &args, void *stream, void *e0, void *e1)
 }
 
 // Partial sums of the weight's gradient: one per block, at most kParts blocks;
-// rows too long for registers are dealt out over as many parts.
+// rows too long for registers are dealt out over as many parts. A block of 16
+// wavefronts has a CU to itself, so more than 256 of them only wait, and write
+// twice the partial sums (256 against 512 blocks: 2048 x 8192 24.3 and 31.1 us,
+// 2048 x 16384 86 and 107, 16384 x 8192 148 and 152; of smaller blocks two
+// share a CU: 16384 x 4096 90 and 80, 8192 x 2048 26.0 and 24.9).
 namespace {
-constexpr int kParts = 512;
+constexpr int kParts = 512, kWideParts = 256;
 }
 
 int norm_backward_parts(int64_t rows, int64_t cols)
 {
     const int waves = row_waves(cols), groups = cols > kRowCols ? 1 : backward_threads(waves) / 64 / waves;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, kParts)));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, waves == 16 && cols <= kRowCols ? kWideParts : kParts)));
 }
 
 int launch_norm_backward(const NormBackArgs &args, void *stream, void *e0, void *end, int *launches)
