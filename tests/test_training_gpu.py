@@ -314,6 +314,33 @@ def test_norm_gradient_against_differences(kind):
     assert abs(got - (loss(h) - loss(-h)) / (2 * h)) <= 1e-6 * size
 
 
+def test_norm_offsets_past_32_bits():
+    rows, cols = (1 << 19) + 5, 4104                 # 2.15e9 elements
+    some = [0, rows // 2 + 1, rows - 2, rows - 1]
+    x = torch.zeros(rows, cols, dtype=BF, device="cuda")
+    x[some] = randn(gen(5), len(some), cols)
+    w = randn(gen(6), 1, cols).float()[0]
+    y, stats, q = torch.empty_like(x), torch.empty(rows, 2, device="cuda"), fp.checkpoint_empty(rows, cols)
+    fp.norm_forward(x, w, y, stats, out_checkpoint=q)
+    # a row's result does not depend on the others
+    y2, stats2, q2 = torch.empty(len(some), cols, dtype=BF, device="cuda"), torch.empty(len(some), 2, device="cuda"), fp.checkpoint_empty(len(some), cols)
+    fp.norm_forward(x[some], w, y2, stats2, out_checkpoint=q2)
+    assert same(y[some], y2) and same(stats[some], stats2) and same(q.scales[some], q2.scales)
+    assert same(q.values.view(torch.uint8)[some], q2.values.view(torch.uint8))
+    # y as dy, and its 8 bits as the backward pass's input: dx beside it
+    dx, dw, dx2 = torch.empty_like(x), torch.empty(cols, device="cuda"), torch.empty_like(y2)
+    del x
+    fp.norm_backward(y, q, w, stats, dx, dw, workspace(fp.norm_backward_workspace(rows, cols)))
+    fp.norm_backward(y2, q2, w, stats2, dx2, None, None)
+    assert same(dx[some], dx2)
+    # rows of zeros add nothing: mean 0 and dy 0
+    xh = (values(q2) - stats2[:, :1].double()) * stats2[:, 1:].double()
+    want, terms = (y2.double() * xh).sum(0), (y2.double() * xh).abs().sum(0)
+    close(dw, want, (len(some) + 6) * U * (terms + (y2.double() * stats2[:, 1:].double()).abs().sum(0)), "dweight")
+    del y, q, dx
+    torch.cuda.empty_cache()
+
+
 def test_norm_non_finite_rows_stay_apart():
     x = torch.randn(8, 200, device="cuda").to(BF)
     x[2, 5] = float("inf")
@@ -556,6 +583,48 @@ def test_gated_backward(act, rows, cols, ffn, kept, x_kind, gdt):
     again = [torch.empty_like(t) for t in (dx, dwg, dwu)]
     fp.gated_backward(dy, ax, wg, wu, ag, au, *again, ws, activation=act)
     assert all(torch.equal(p, q) for p, q in zip(again, (dx, dwg, dwu)))
+
+
+# Few rows and the tiles with weights of over 2^31 elements, and kept
+# activations of as many; everything is zero but a few rows and one column.
+@pytest.mark.parametrize("rows,cols,ffn", [(3, 2056, (1 << 20) + 8), (40, 2056, (1 << 20) + 8), ((1 << 16) + 8, 64, (1 << 15) + 8)])
+def test_gated_offsets_past_32_bits(rows, cols, ffn):
+    some = [0, rows // 2, rows - 1]
+    x = torch.zeros(rows, cols, dtype=BF, device="cuda")
+    x[some, -1] = torch.tensor([1.0, -0.5, 2.0], dtype=BF, device="cuda")
+    wg, wu = (torch.zeros(ffn, cols, dtype=BF, device="cuda") for _ in range(2))
+    f = torch.arange(ffn, device="cuda")
+    wg[:, -1], wu[:, -1] = (f % 3 + 1).to(BF), (f % 5 - 2).to(BF)
+    h, gate, up = (torch.full((rows, ffn), float("nan"), dtype=BF, device="cuda") for _ in range(3))
+    fp.gated_forward(x, wg, wu, h, gate=gate, up=up)
+    xs, g1, u1 = x[some, -1].double(), wg[:, -1].double(), wu[:, -1].double()
+    G, Up = xs[:, None] * g1, xs[:, None] * u1       # exact: products of small numbers
+    assert torch.equal(gate[some].double(), G) and torch.equal(up[some].double(), Up)
+    act, dact = act_reference(fp.SILU, G)
+    hh = act * Up
+    close(h[some], hh, ACT * (G.abs() + 1) * Up.abs() * 1.01 + half[BF] * hh.abs() * 1.01, "out")
+    for t in (h, gate, up):
+        assert int((t != 0).any(1).sum()) == len(some)
+    # back: h as the gradient of itself
+    dx = torch.full((rows, cols), float("nan"), device="cuda")
+    dwg, dwu = (torch.full((ffn, cols), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    fp.gated_backward(h, x, wg, wu, gate, up, dx, dwg, dwu, workspace(fp.gated_backward_workspace(rows, ffn, cols)))
+    d = h[some].double()
+    dg, du = d * Up * dact, d * act
+    eg = ACT * 4 * (G.abs() + 1) * Up.abs() * d.abs() * 1.01 + half[BF] * dg.abs() * 1.01
+    eu = ACT * (G.abs() + 1) * d.abs() * 1.01 + half[BF] * du.abs() * 1.01
+    want = dg @ g1 + du @ u1
+    bound = eg @ g1 + eu @ u1.abs()
+    bound = bound + (2 * ffn + 2) * U * ((dg.abs() + eg) @ g1 + (du.abs() + eu) @ u1.abs())
+    close(dx[some, -1], want, bound, "dx")
+    assert int((dx != 0).sum()) <= len(some) and not bool(dx[:, :-1].any())
+    for got, v, e in ((dwg, dg, eg), (dwu, du, eu)):
+        want = v.t().contiguous() @ xs
+        bound = e.t().contiguous() @ xs.abs() + 4 * U * ((v.abs() + e).t().contiguous() @ xs.abs())
+        close(got[:, -1], want, bound + half[BF] * (want.abs() + bound), "dw")
+        assert int((got != 0).any(0).sum()) == 1
+    del h, gate, up, wg, wu, dwg, dwu
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("act", [fp.SILU, fp.GELU_TANH])
