@@ -679,19 +679,23 @@ int launch_norm_forward(const NormArgs &args, void *stream, void *e0, void *e1)
 }
 
 // Partial sums of the weight's gradient: one per block, at most kParts blocks;
-// rows too long for registers are dealt out over as many parts. A block of 16
-// wavefronts has a CU to itself, so more than 256 of them only wait, and write
-// twice the partial sums (256 against 512 blocks: 2048 x 8192 24.3 and 31.1 us,
-// 2048 x 16384 86 and 107, 16384 x 8192 148 and 152; of smaller blocks two
-// share a CU: 16384 x 4096 90 and 80, 8192 x 2048 26.0 and 24.9).
+// rows too long for registers are dealt out over as many parts. Half as many
+// where a block of 16 wavefronts has a CU to itself and more only wait (256
+// against 512 blocks: 2048 x 8192 24.3 and 31.1 us, 2048 x 16384 86 and 107,
+// 16384 x 8192 148 and 152), and where there is so little to read that starting
+// blocks and joining their sums counts (512 x 4096 12.6 and 16.5 us, 4099 x 1001
+// 13.2 and 14.5, 8192 x 512 11.2 and 12.0, 2048 x 4096 17.3 and 18.2). Else two
+// blocks share a CU: 4096 x 4096 25.9 and 24.4, 16384 x 1024 24.4 and 22.3.
 namespace {
-constexpr int kParts = 512, kWideParts = 256;
+constexpr int kParts = 512;
+constexpr int64_t kFewElements = 12 << 20;
 }
 
 int norm_backward_parts(int64_t rows, int64_t cols)
 {
     const int waves = row_waves(cols), groups = cols > kRowCols ? 1 : backward_threads(waves) / 64 / waves;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, waves == 16 && cols <= kRowCols ? kWideParts : kParts)));
+    const int most = cols <= kRowCols && (waves == 16 || rows * cols < kFewElements) ? kParts / 2 : kParts;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, most)));
 }
 
 int launch_norm_backward(const NormBackArgs &args, void *stream, void *e0, void *end, int *launches)
